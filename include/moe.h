@@ -420,6 +420,167 @@ int moe_quantize_act_q8(const void *src, int32_t src_format, int64_t rows, int32
  * MOE_ERR_HIP. */
 int moe_bias_update(int32_t E, const int32_t *counts, float *router_bias, float gamma, void *stream);
 
+/* ==== the rest of a decoder layer: projections, cache and attention ====
+ *
+ * The calls below make the half of a decoder layer that runs before the MoE
+ * layer: few-token projections with packed int4 weights and group scales
+ * (moe_linear_q4), appending keys and values to a paged cache with the per-head
+ * norm and the position rotation on the way (moe_kv_append), and attention over
+ * that cache (moe_kv_attention).  The pages name grouped heads with a per-head
+ * norm of q and k (Colibri-Nano model card, "Architecture"), an int8 key/value
+ * cache (colibri-nano README, "Knobs": KV_I8) and int4 containers, and give no
+ * layouts; the layouts here are this library's.  The conventions at the top of
+ * this file hold: device pointers, nothing allocated, nothing read back, errors
+ * before anything is enqueued, deterministic results.
+ *
+ * Cache of one layer, P = page_tokens, D = head_dim, page ids from the caller:
+ *   k  [n_pages][kv_heads][P][D],  v  [n_pages][kv_heads][D][P]   (v transposed)
+ *   kv_bits 16: bf16 values.
+ *   kv_bits 8:  int8 codes, a value is code * scale with one f32 scale per page
+ *               and head, k_scale and v_scale [n_pages][kv_heads].  A page gets
+ *               its codes once, when its last row comes: scale = max|v| / 127 over
+ *               the page's P x D values of the head (f32, correctly rounded), code
+ *               = nearest integer to v / scale, ties to even; an all-zero page has
+ *               scale 0 and codes 0; a page with an infinity or NaN gets a NaN
+ *               scale and reads as NaN.  Until then its rows stay in bf16 in the
+ *               sequence's open pages, which the caller also owns:
+ *               k_tail [n_slots][2][kv_heads][P][D], v_tail [n_slots][2][kv_heads][D][P],
+ *               page i of the sequence in half i % 2 of its slot.  So the stored
+ *               values do not depend on how the tokens were cut into appends, and
+ *               the rows of the two newest pages are always there in bf16: the last
+ *               P tokens can be dropped (drafted tokens that were refused) by
+ *               passing a smaller kv_len.
+ * Row i of sequence s is row row_start[s] + i of the batch's tensors; with n_s =
+ * row_start[s+1] - row_start[s] rows it has position kv_len[s] - n_s + i, kv_len
+ * counting the new rows.  Position p lives in page pages[s][p / P], row p % P.  A
+ * page id outside [0, n_pages) marks an absent page (one not there yet or
+ * given back): nothing is written to it and its tokens are not seen.  The same
+ * goes for an open page of a slot outside [0, n_slots).
+ * The device tables are not checked on the host; the kernels keep every access
+ * inside the sizes of the shape whatever the tables hold.
+ */
+#define MOE_KV_NONCAUSAL 0x10000u  /* moe_kv_attention: rows see the whole sequence, later positions too */
+#define MOE_KV_ROPE_PAIRS 0x20000u /* moe_kv_append: rotate adjacent pairs (2j, 2j+1); otherwise (j, j + rot_dim/2) */
+
+typedef struct {
+    int32_t n_seq;       /* sequences of the batch, >= 0 */
+    int32_t rows;        /* rows (new tokens) of all sequences, >= 0 */
+    int32_t max_rows;    /* no sequence has more rows than this (rows beyond it are left out), 0..rows */
+    int32_t max_len;     /* no kv_len is above this (positions from it on are left out), >= 0 */
+    int32_t q_heads, kv_heads; /* q head h reads key/value head h / (q_heads / kv_heads) */
+    int32_t head_dim;    /* 64 or 128 */
+    int32_t kv_bits;     /* 8 or 16 */
+    int32_t page_tokens; /* 16, 32, 64 or 128 */
+    int32_t n_pages;     /* pages of the cache */
+    int32_t max_pages;   /* row length of the page table */
+    int32_t n_slots;     /* kv_bits 8: sequences that have open pages */
+    int32_t window;      /* > 0: a row at position p sees positions above p - window only; 0: all */
+    float scale;         /* scores are scale * q.k; 0: 1 / sqrt(head_dim) */
+    uint32_t flags;      /* MOE_KV_NONCAUSAL, MOE_KV_ROPE_PAIRS, MOE_OUT_F32 */
+} moe_kv_shape;
+
+typedef struct {
+    const int32_t *row_start; /* [n_seq + 1], ascending */
+    const int32_t *kv_len;    /* [n_seq] */
+    const int32_t *pages;     /* [n_seq][max_pages] */
+    const int32_t *slots;     /* [n_seq], kv_bits 8; NULL: sequence s has slot s */
+} moe_kv_batch;
+
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;  /* kv_bits 8 */
+    moe_bf16 *k_tail, *v_tail; /* kv_bits 8 */
+} moe_kv_cache;
+
+typedef struct {
+    const float *cos, *sin; /* [n_pos][rot_dim / 2]; not read when rot_dim == 0 */
+    int32_t n_pos;          /* a row whose position is outside the table gets NaN in its rotated part */
+    int32_t rot_dim;        /* the first rot_dim values of each head are rotated; 0..head_dim, a multiple of 16 */
+    const int32_t *pos;     /* [rows] positions in the table; NULL: the cache positions */
+    const float *q_norm, *k_norm; /* [head_dim] RMS-norm weights of q and k heads, each nullable (no norm) */
+    float eps;              /* x * rsqrt(mean(x^2) + eps) * norm */
+} moe_kv_rotary;
+
+/*
+ * moe_kv_append -- store the batch's new keys and values, and rotate its queries.
+ *   k, v  [rows][kv_heads][head_dim] bf16, rows k_row_stride / v_row_stride elements
+ *         apart (so a fused projection's slices can be passed): k is normed per head,
+ *         rotated by its position ((a, b) -> (a cos - b sin, a sin + b cos), computed
+ *         in f32), rounded to bf16 and stored; v is stored as it is
+ *   q     nullable, [rows][q_heads][head_dim] bf16, row stride q_row_stride: normed and
+ *         rotated like k into q_out [rows][q_heads][head_dim], which may be q itself
+ *   rot   nullable: no norm and no rotation
+ * Different sequences of a call must not share a page that the call writes, or a slot.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (head_dim, page_tokens or
+ * rot_dim the kernels do not cover), MOE_ERR_ALIGN (pointers to 16 bytes, tables to 4;
+ * row strides to 8 elements), MOE_ERR_HIP.  rows == 0 is a no-op.
+ */
+int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache,
+                  const moe_kv_rotary *rot, const moe_bf16 *k, int64_t k_row_stride, const moe_bf16 *v,
+                  int64_t v_row_stride, const moe_bf16 *q, int64_t q_row_stride, moe_bf16 *q_out, void *stream);
+
+/*
+ * moe_kv_attention -- attention of the batch's rows over the cache.
+ * For row i of sequence s at position p and query head h, over the positions j < kv_len[s]
+ * that the row sees (j <= p unless MOE_KV_NONCAUSAL; j > p - window with a window; page
+ * present):
+ *   z_j = scale * q.k_j,  m = max z,  l = sum exp(z_j - m),
+ *   out = sum_j exp(z_j - m) v_j / l,  lse = m + log l.
+ * A row that sees nothing gets out 0 and lse -infinity.  Products run on the matrix
+ * cores with f32 accumulation: q, keys and int8 codes are exact in bf16, and each weight
+ * exp(z_j - m) is rounded to 16 bits for the product with the values (2^-8 relative or
+ * better) while l, m and all sums stay in f32.  Positions from kv_len on are never used;
+ * a value that is infinite or NaN at a position some row of the call sees may
+ * reach other rows of the same sequence and head.
+ *   q    [rows][q_heads][head_dim] bf16, row stride q_row_stride (moe_kv_append's q_out)
+ *   out  [rows][q_heads][head_dim] bf16, or f32 with MOE_OUT_F32
+ *   lse  nullable, [rows][q_heads] f32 (natural log)
+ *   ws   moe_kv_workspace_bytes(shape) bytes, 256-byte aligned (parts of a long sequence)
+ * Errors as moe_kv_append, and MOE_ERR_WORKSPACE.
+ */
+int moe_kv_attention(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache,
+                     const moe_bf16 *q, int64_t q_row_stride, void *out, float *lse, void *ws, size_t ws_bytes,
+                     void *stream);
+
+/* Bytes of workspace moe_kv_attention needs for this shape (0 for an invalid shape, at
+ * least 256 otherwise).  It grows with rows, q_heads and, below a bound, max_len. */
+size_t moe_kv_workspace_bytes(const moe_kv_shape *shape);
+
+/*
+ * moe_kv_read -- the stored values of the batch's rows: what the cache holds at the last
+ * n_s = row_start[s+1] - row_start[s] positions of each sequence, for looking at a cache,
+ * moving it or checking it.  k, v [rows][kv_heads][head_dim] bf16 (code * scale rounded to
+ * nearest even in 8 bits); positions below 0 and absent pages read as 0.
+ */
+int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache, moe_bf16 *k,
+                moe_bf16 *v, void *stream);
+
+/*
+ * moe_linear_q4 -- y = x W^T for a few tokens, W packed int4 with group scales:
+ *   out[t][n] = sum over groups g of scales[n][g] * sum_{k in g} x[t][k] * code[n][k]
+ *               (+ residual[t][n]),
+ * products exact on the matrix cores, all sums in f32, rounded once at the end.
+ *   x         [T][K] bf16, row stride x_row_stride elements
+ *   q         [N][K/2] bytes, codes packed as everywhere in this file: what
+ *             moe_quantize_rows(rows = N * K / group, cols = group, bits 4) writes
+ *   scales    [N][K/group] f32 (MOE_SRC_F32: that call's scales) or bf16 (MOE_SRC_BF16)
+ *   residual  nullable, [T][N] bf16; may be out itself when out is bf16
+ *   out       [T][N] bf16, or f32 with flags & MOE_OUT_F32
+ *   ws        moe_linear_q4_workspace_bytes(T, N, K) bytes, 256-byte aligned
+ * group is 32, 64 or 128 and divides K; any N and T (made for T <= 64: a larger batch
+ * reads the weights again for every 64 tokens).
+ * Errors: MOE_ERR_SHAPE (negative sizes, K % group, a format or stride out of range),
+ * MOE_ERR_UNSUPPORTED (group), MOE_ERR_NULL, MOE_ERR_ALIGN (x, q, scales, ws; residual and
+ * out to their elements; x_row_stride % 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or
+ * N == 0 is a no-op.
+ */
+int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, const moe_bf16 *x, int64_t x_row_stride,
+                  const void *q, const void *scales, int32_t scale_format, const moe_bf16 *residual, void *out,
+                  uint32_t flags, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_linear_q4 needs (0 for invalid sizes, at least 256 otherwise). */
+size_t moe_linear_q4_workspace_bytes(int32_t T, int32_t N, int32_t K);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,8 +7,11 @@ library is missing, every call raises -- there is no CPU fallback.
 The functions mirror the C ABI names:
   moe_router, moe_permute, moe_expert_ffn, moe_combine, moe_layer_forward,
   moe_workspace_bytes, moe_validate_shape, moe_status_string, moe_layer_routing,
-  moe_quantize_rows, moe_bias_update, moe_layer_forward_chain, moe_quantize_act_q8
-and ``MoeLayer`` keeps one layer's device weights and workspace.
+  moe_quantize_rows, moe_bias_update, moe_layer_forward_chain, moe_quantize_act_q8,
+  moe_kv_append, moe_kv_attention, moe_kv_read, moe_kv_workspace_bytes,
+  moe_linear_q4, moe_linear_q4_workspace_bytes
+and ``MoeLayer`` keeps one layer's device weights and workspace, ``KvPages`` one
+layer's key/value cache.
 """
 from __future__ import annotations
 
@@ -39,6 +42,9 @@ MOE_EXPERT_MIXED = 0x2000
 MOE_REGIME_TILED = 0x4000
 MOE_REGIME_SMALL = 0x8000
 
+MOE_KV_NONCAUSAL = 0x10000
+MOE_KV_ROPE_PAIRS = 0x20000
+
 MOE_SRC_F32 = 0
 MOE_SRC_BF16 = 1
 
@@ -49,7 +55,8 @@ MOE_WS_LAYER = 3
 EXPORTS = ["moe_router", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_forward_profiled", "moe_workspace_bytes", "moe_validate_shape", "moe_status_string",
            "moe_layer_routing", "moe_quantize_rows", "moe_bias_update", "moe_layer_forward_chain",
-           "moe_quantize_act_q8", "moe_layer_forward_noalloc"]
+           "moe_quantize_act_q8", "moe_layer_forward_noalloc", "moe_kv_append", "moe_kv_attention", "moe_kv_read",
+           "moe_kv_workspace_bytes", "moe_linear_q4", "moe_linear_q4_workspace_bytes"]
 
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -73,6 +80,30 @@ class MoeWeights(ctypes.Structure):
                 ("sh_gate", MoeQMat), ("sh_up", MoeQMat), ("sh_down", MoeQMat), ("expert_bits", ctypes.c_void_p)]
 
 
+class MoeKvShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("kv_bits", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class MoeKvBatch(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p)]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p)]
+
+
+class MoeKvRotary(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("pos", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -91,7 +122,8 @@ def load() -> ctypes.CDLL:
                               "(hipcc --offload-arch=gfx950); there is no fallback path")
         L = ctypes.CDLL(LIB_PATH)
         vp, S, W = ctypes.c_void_p, ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights)
-        sz = ctypes.c_size_t
+        sz, i32, i64 = ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
+        KS, KB, KC = ctypes.POINTER(MoeKvShape), ctypes.POINTER(MoeKvBatch), ctypes.POINTER(MoeKvCache)
         sig = {
             "moe_router": [S, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_permute": [S, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -106,6 +138,10 @@ def load() -> ctypes.CDLL:
             "moe_quantize_rows": [vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
             "moe_quantize_act_q8": [vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, vp, vp, vp],
             "moe_bias_update": [ctypes.c_int32, vp, vp, ctypes.c_float, vp],
+            "moe_kv_append": [KS, KB, KC, ctypes.POINTER(MoeKvRotary), vp, i64, vp, i64, vp, i64, vp, vp],
+            "moe_kv_attention": [KS, KB, KC, vp, i64, vp, vp, vp, sz, vp],
+            "moe_kv_read": [KS, KB, KC, vp, vp, vp],
+            "moe_linear_q4": [i32, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp, ctypes.c_uint32, vp, sz, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -113,6 +149,10 @@ def load() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         L.moe_workspace_bytes.argtypes = [S, ctypes.c_int]
         L.moe_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_kv_workspace_bytes.argtypes = [KS]
+        L.moe_kv_workspace_bytes.restype = sz
+        L.moe_linear_q4_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_linear_q4_workspace_bytes.restype = sz
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -275,6 +315,191 @@ def moe_bias_update(counts, router_bias, gamma: float, stream=None):
         raise ValueError("counts and router_bias must both have E elements")
     _check(load().moe_bias_update(router_bias.numel(), _ptr(counts), _ptr(router_bias), gamma, _stream(stream)),
            "moe_bias_update")
+
+
+# ---- the rest of a decoder layer: projections, cache, attention (include/moe.h)
+
+
+def kv_shape(n_seq, rows, max_rows, max_len, q_heads, kv_heads, head_dim, kv_bits=8, page_tokens=64, n_pages=0,
+             max_pages=0, n_slots=0, window=0, scale=0.0, flags=0) -> MoeKvShape:
+    return MoeKvShape(n_seq, rows, max_rows, max_len, q_heads, kv_heads, head_dim, kv_bits, page_tokens, n_pages,
+                      max_pages, n_slots, window, scale, flags)
+
+
+def _typed(t, dtype, what):
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    return _ptr(t)
+
+
+def kv_batch(row_start, kv_len, pages, slots=None) -> MoeKvBatch:
+    """The batch's device tables (int32): row_start [n_seq + 1], kv_len [n_seq], pages [n_seq][max_pages], slots
+    [n_seq] or None.  The struct keeps the tensors alive."""
+    import torch
+    b = MoeKvBatch(*(_typed(t, torch.int32, "the batch's tables") for t in (row_start, kv_len, pages, slots)))
+    b.tensors = (row_start, kv_len, pages, slots)
+    b.sizes = (row_start.numel(), kv_len.numel(), tuple(pages.shape), slots.numel() if slots is not None else None)
+    return b
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None, k_tail=None, v_tail=None) -> MoeKvCache:
+    """One layer's cache tensors: int8 codes with f32 scales and bf16 open pages, or bf16 k and v alone.  The struct
+    keeps the tensors alive."""
+    import torch
+    codes = torch.int8 if k_scale is not None else torch.bfloat16
+    c = MoeKvCache(_typed(k, codes, "k"), _typed(v, codes, "v"), _typed(k_scale, torch.float32, "k_scale"),
+                   _typed(v_scale, torch.float32, "v_scale"), _typed(k_tail, torch.bfloat16, "k_tail"),
+                   _typed(v_tail, torch.bfloat16, "v_tail"))
+    c.tensors = (k, v, k_scale, v_scale, k_tail, v_tail)
+    c.sizes = tuple(tuple(t.shape) if t is not None else None for t in c.tensors)
+    return c
+
+
+def _kv_fits(sh, batch, cache):
+    """The tensors are as large as the shape says (the library sees only their addresses)."""
+    n, pages = sh.n_seq, (sh.n_seq, sh.max_pages)
+    starts, lens, table, slots = batch.sizes
+    if starts < n + 1 or lens < n or table != pages or (slots is not None and slots < n):
+        raise ValueError("the batch's tables do not fit the shape")
+    h, p, d = sh.kv_heads, sh.page_tokens, sh.head_dim
+    want = ((sh.n_pages, h, p, d), (sh.n_pages, h, d, p))
+    if sh.kv_bits == 8:
+        want += ((sh.n_pages, h), (sh.n_pages, h), (sh.n_slots, 2, h, p, d), (sh.n_slots, 2, h, d, p))
+        if slots is None and sh.n_slots < n:
+            raise ValueError("n_slots is below n_seq and no slots are given")
+    else:
+        want += (None,) * 4
+    if cache.sizes != want:
+        raise ValueError("the cache's tensors do not fit the shape")
+
+
+def kv_rotary(cos=None, sin=None, rot_dim=0, pos=None, q_norm=None, k_norm=None, eps=1e-6) -> MoeKvRotary:
+    """Position tables cos and sin [n_pos][rot_dim / 2] (f32), positions pos [rows] (int32) or None for the cache's
+    own, and the per-head norm weights (f32 [head_dim]) of q and k, each or None."""
+    import torch
+    for t in (cos, sin):
+        if rot_dim and (t is None or t.dim() != 2 or t.shape != cos.shape or t.shape[1] * 2 != rot_dim):
+            raise ValueError("cos and sin must be [n_pos][rot_dim / 2]")
+    r = MoeKvRotary(_typed(cos, torch.float32, "cos"), _typed(sin, torch.float32, "sin"),
+                    cos.shape[0] if cos is not None else 0, rot_dim, _typed(pos, torch.int32, "pos"),
+                    _typed(q_norm, torch.float32, "q_norm"), _typed(k_norm, torch.float32, "k_norm"), eps)
+    r.tensors = (cos, sin, pos, q_norm, k_norm)
+    r.sizes = tuple(t.numel() if t is not None else None for t in (pos, q_norm, k_norm))
+    return r
+
+
+def _head_rows(t, rows, heads, dim, what):
+    """Pointer and row stride of a [rows][heads][dim] bf16 tensor whose rows may be apart."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{what} must be a bfloat16 GPU tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what} must be [{rows}][{heads}][{dim}]")
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    return t.data_ptr(), stride[0] if rows > 1 else heads * dim
+
+
+def _head_out(t, rows, heads, dim, what, f32=False):
+    import torch
+    if t.dtype != (torch.float32 if f32 else torch.bfloat16) or tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{what} must be a {'float32' if f32 else 'bfloat16'} [{rows}][{heads}][{dim}] tensor")
+    return _ptr(t)
+
+
+def moe_kv_workspace_bytes(sh: MoeKvShape) -> int:
+    return int(load().moe_kv_workspace_bytes(ctypes.byref(sh)))
+
+
+def moe_kv_append(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, rot: Optional[MoeKvRotary] = None,
+                  q=None, q_out=None, stream=None):
+    """Store the batch's keys and values (norm and rotation of k on the way) and rotate q into q_out (include/moe.h).
+    k, v [rows][kv_heads][head_dim] and q [rows][q_heads][head_dim] bf16, rows possibly apart."""
+    _kv_fits(sh, batch, cache)
+    if rot is not None and (rot.sizes[0] not in (None, sh.rows) or rot.sizes[1] not in (None, sh.head_dim) or
+                            rot.sizes[2] not in (None, sh.head_dim)):
+        raise ValueError("pos must be [rows], q_norm and k_norm [head_dim]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    kp, ks = _head_rows(k, sh.rows, sh.kv_heads, sh.head_dim, "k")
+    vp, vs = _head_rows(v, sh.rows, sh.kv_heads, sh.head_dim, "v")
+    qp, qs = _head_rows(q, sh.rows, sh.q_heads, sh.head_dim, "q") if q is not None else (None, 0)
+    qo = _head_out(q_out, sh.rows, sh.q_heads, sh.head_dim, "q_out") if q_out is not None else None
+    _check(load().moe_kv_append(sh, batch, cache, rot, kp, ks, vp, vs, qp, qs, qo, _stream(stream)), "moe_kv_append")
+
+
+def moe_kv_attention(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, q, out, lse=None, ws=None, stream=None):
+    """Attention of the batch's rows over the cache (include/moe.h): out [rows][q_heads][head_dim] (bf16, or f32 with
+    MOE_OUT_F32), lse [rows][q_heads] f32 or None, ws moe_kv_workspace_bytes(sh) bytes."""
+    import torch
+    _kv_fits(sh, batch, cache)
+    qp, qs = _head_rows(q, sh.rows, sh.q_heads, sh.head_dim, "q")
+    op = _head_out(out, sh.rows, sh.q_heads, sh.head_dim, "out", bool(sh.flags & MOE_OUT_F32))
+    if lse is not None and lse.numel() != sh.rows * sh.q_heads:
+        raise ValueError("lse must be [rows][q_heads]")
+    _check(load().moe_kv_attention(sh, batch, cache, qp, qs, op, _typed(lse, torch.float32, "lse"), _ptr(ws),
+                                   ws.numel() if ws is not None else 0, _stream(stream)), "moe_kv_attention")
+
+
+def moe_kv_read(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, stream=None):
+    """The stored values of the batch's rows (include/moe.h) into k, v [rows][kv_heads][head_dim] bf16."""
+    _kv_fits(sh, batch, cache)
+    kp = _head_out(k, sh.rows, sh.kv_heads, sh.head_dim, "k")
+    vp = _head_out(v, sh.rows, sh.kv_heads, sh.head_dim, "v")
+    _check(load().moe_kv_read(sh, batch, cache, kp, vp, _stream(stream)), "moe_kv_read")
+
+
+def moe_linear_q4_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(load().moe_linear_q4_workspace_bytes(T, N, K))
+
+
+def moe_linear_q4(x, q, scales, out, residual=None, ws=None, stream=None):
+    """out = x W^T (+ residual) for a few tokens, W packed int4 with group scales (include/moe.h): x [T][K] bf16 (rows
+    possibly apart), q uint8 [N][K/2], scales f32 or bf16 [N][K/group], out [T][N] bf16 or f32."""
+    import torch
+    T, K = x.shape
+    N = q.shape[0]
+    if x.dtype != torch.bfloat16 or not x.is_cuda or (x.numel() and x.stride(1) != 1):
+        raise ValueError("x must be a bfloat16 GPU tensor with contiguous rows")
+    if tuple(q.shape) != (N, K // 2) or q.dtype not in (torch.uint8, torch.int8):
+        raise ValueError("q must be [N][K/2] bytes")
+    if scales.dim() != 2 or scales.shape[0] != N or scales.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("scales must be [N][K/group] float32 or bfloat16")
+    if tuple(out.shape) != (T, N) or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be [T][N] float32 or bfloat16")
+    if residual is not None and (tuple(residual.shape) != (T, N) or residual.dtype != torch.bfloat16):
+        raise ValueError("residual must be a bfloat16 [T][N] tensor")
+    if scales.shape[1] == 0 or K % scales.shape[1]:
+        raise ValueError("scales must be [N][K/group] with group dividing K")
+    _check(load().moe_linear_q4(T, N, K, K // scales.shape[1], x.data_ptr(), x.stride(0) if T > 1 else K, _ptr(q),
+                                _ptr(scales), MOE_SRC_F32 if scales.dtype == torch.float32 else MOE_SRC_BF16,
+                                _ptr(residual), _ptr(out), MOE_OUT_F32 if out.dtype == torch.float32 else 0, _ptr(ws),
+                                ws.numel() if ws is not None else 0, _stream(stream)), "moe_linear_q4")
+
+
+class KvPages:
+    """One layer's key/value cache on the device, in the layout of include/moe.h, and its handle for the calls."""
+
+    def __init__(self, n_pages, kv_heads, head_dim, page_tokens=64, kv_bits=8, n_slots=0, device="cuda"):
+        import torch
+        dt = torch.int8 if kv_bits == 8 else torch.bfloat16
+        shape_k, shape_v = (kv_heads, page_tokens, head_dim), (kv_heads, head_dim, page_tokens)
+        self.k = torch.empty((n_pages, *shape_k), dtype=dt, device=device)
+        self.v = torch.empty((n_pages, *shape_v), dtype=dt, device=device)
+        self.k_scale = self.v_scale = self.k_tail = self.v_tail = None
+        if kv_bits == 8:
+            self.k_scale = torch.empty((n_pages, kv_heads), dtype=torch.float32, device=device)
+            self.v_scale = torch.empty((n_pages, kv_heads), dtype=torch.float32, device=device)
+            self.k_tail = torch.empty((n_slots, 2, *shape_k), dtype=torch.bfloat16, device=device)
+            self.v_tail = torch.empty((n_slots, 2, *shape_v), dtype=torch.bfloat16, device=device)
+        self.handle = kv_cache(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
+        self.sizes = dict(kv_heads=kv_heads, head_dim=head_dim, kv_bits=kv_bits, page_tokens=page_tokens,
+                          n_pages=n_pages, n_slots=n_slots)
+
+    def shape(self, n_seq, rows, max_rows, max_len, q_heads, max_pages, **kw) -> MoeKvShape:
+        return kv_shape(n_seq=n_seq, rows=rows, max_rows=max_rows, max_len=max_len, q_heads=q_heads,
+                        max_pages=max_pages, **self.sizes, **kw)
 
 
 def qmat(q, qs, q_stride_bytes: int = 0, qs_stride_floats: int = 0, q_offset: int = 0, qs_offset: int = 0) -> MoeQMat:

@@ -1,0 +1,453 @@
+// kv_append.hip -- new keys and values into the paged cache, with the per-head
+// norm and the position rotation on the way; and the stored values back.
+//
+// A head of one row is x (D values).  With a norm, y = x * rsqrt(mean x^2 + eps)
+// * w; the first R values are rotated, (a, b) -> (a c - b s, a s + b c) with c, s
+// of the row's position; the result is rounded to bf16 once.  In 8 bits a page
+// of one head (P x D values) gets scale = max|v| / 127 and codes rint(v / scale)
+// when its last row comes, from the bf16 values, so the codes are the same
+// however the rows arrived.
+//
+// One workgroup per (sequence, touched page, head, k or v): a page's codes need
+// all its rows anyway, and this is also the unit that a transposed store (v is
+// [D][P]) wants in LDS.  Eight values of a row per lane (16-byte loads); D / 8
+// lanes hold a row, so the norm's sum is a butterfly over them.  Queries take
+// the same arithmetic in workgroups of the same launch.  What bounds it: HBM for
+// prompts (each value read once, written once, the older rows of the one partial
+// page read again), the launch itself for a decode step.
+#include "kv_device.h"
+
+namespace moe {
+
+constexpr int KVA_THREADS = 256;
+
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 r = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Eight values at element e of a head (16-byte aligned) after norm and
+// rotation, in bf16.  All D / 8 lanes of the row call it together.
+template <int D>
+__device__ __forceinline__ u32x4 normed_rotated(const uint16_t *head, int e, const float *norm, const KvAppend &n,
+                                                int pos)
+{
+    const u32x4 raw = *(const u32x4 *)(head + e);
+    const bool rotated = e < n.rot_dim;
+    if (!norm && !rotated) return raw;
+    const int half = n.rot_dim >> 1;
+    const int pe = n.pairs || !rotated ? e : e < half ? e + half : e - half;  // the partners' place
+    const u32x4 praw = *(const u32x4 *)(head + pe);
+    float x[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(raw[i]);
+        x[2 * i + 1] = bf16_hi(raw[i]);
+        y[2 * i] = bf16_lo(praw[i]);
+        y[2 * i + 1] = bf16_hi(praw[i]);
+    }
+    if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor(ss, o, WAVE);
+        const float r = rsqrtf(ss * (1.0f / D) + n.eps);
+        const f32x4 *w = (const f32x4 *)(norm + e), *pw = (const f32x4 *)(norm + pe);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] * r * w[i / 4][i % 4];
+            y[i] = y[i] * r * pw[i / 4][i % 4];
+        }
+    }
+    if (rotated) {
+        const bool in_table = (unsigned)pos < (unsigned)n.n_pos;
+        const int64_t row = (int64_t)(in_table ? pos : 0) * half;
+        if (n.pairs) {
+            f32x4 c, s;
+            if (in_table) {
+                c = *(const f32x4 *)(n.cos + row + e / 2);
+                s = *(const f32x4 *)(n.sin + row + e / 2);
+            } else {
+                c = s = f32x4{NAN, NAN, NAN, NAN};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = a * c[i] - b * s[i];
+                x[2 * i + 1] = a * s[i] + b * c[i];
+            }
+        } else {
+            const bool first = e < half;
+            const int j = first ? e : e - half;
+            f32x4 c[2], s[2];
+            if (in_table) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    c[i] = *(const f32x4 *)(n.cos + row + j + 4 * i);
+                    s[i] = *(const f32x4 *)(n.sin + row + j + 4 * i);
+                }
+            } else {
+                c[0] = c[1] = s[0] = s[1] = f32x4{NAN, NAN, NAN, NAN};
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = y[i] * s[i / 4][i % 4];
+                x[i] = x[i] * c[i / 4][i % 4] + (first ? -t : t);
+            }
+        }
+    }
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = to_bf16x2(x[2 * i], x[2 * i + 1]);
+    return r;
+}
+
+// The largest |value| of eight bf16 as its bits: NaN above infinity above the
+// finite values, so a page's maximum keeps them.
+__device__ __forceinline__ uint32_t abs_bits_max(uint32_t m, u32x4 v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+    return m;
+}
+
+// A page of one head in LDS, [P][D + 2] bf16: rows are written along D; the
+// extra dword a row puts the 16-row groups that a transposed read takes
+// together on different banks.
+template <int D>
+struct PageTile {
+    static constexpr int ROW = D + 2;
+    uint16_t *t;
+    __device__ void put(int row, int e, u32x4 v) const
+    {
+        uint32_t *p = (uint32_t *)(t + row * ROW + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = v[i];
+    }
+    __device__ u32x4 get(int row, int e) const
+    {
+        const uint32_t *p = (const uint32_t *)(t + row * ROW + e);
+        return u32x4{p[0], p[1], p[2], p[3]};
+    }
+};
+
+// Columns [lo, hi) of a page's transposed values: dst [D][P] at rows d, from
+// the tile.  Whole groups of eight tokens are stored as vectors.
+template <int D>
+__device__ __forceinline__ void store_transposed(uint16_t *dst, int log2p, PageTile<D> tile, int lo, int hi)
+{
+    const int c0 = lo >> 3, nc = ((hi + 7) >> 3) - c0;
+    for (int i = threadIdx.x; i < nc * D; i += KVA_THREADS) {
+        const int d = i / nc, c = c0 + i - d * nc;
+        uint16_t *out = dst + ((int64_t)d << log2p) + c * 8;
+        if (c * 8 >= lo && c * 8 + 8 <= hi) {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = (uint32_t)tile.t[(c * 8 + 2 * j) * tile.ROW + d] |
+                       ((uint32_t)tile.t[(c * 8 + 2 * j + 1) * tile.ROW + d] << 16);
+            }
+            *(u32x4 *)out = v;
+        } else {
+            for (int j = 0; j < 8; ++j)
+                if (c * 8 + j >= lo && c * 8 + j < hi) out[j] = tile.t[(c * 8 + j) * tile.ROW + d];
+        }
+    }
+}
+
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void append_page(const KvArgs &a, const KvAppend &n, int s, int t, int h, uint16_t *lds,
+                                            uint32_t *red)
+{
+    constexpr int LPR = D / 8, RPP = KVA_THREADS / LPR;  // lanes a row, rows a pass
+    const KvSeq sq = kv_seq(a, s);
+    const int L = kv_limit(a, sq), start = sq.len - sq.n_pos, log2p = a.page_log2, P = 1 << log2p;
+    // this call's rows that have a place: positions [lo_all, hi_all)
+    const int lo_all = max(start, 0), hi_all = min(L, start + sq.n);
+    if (hi_all <= lo_all) return;
+    const int first = lo_all >> log2p, last = (hi_all - 1) >> log2p, page = first + t;
+    if (page > last) return;
+    const int id = kv_page(a, s, page), slot = BITS == 8 ? kv_slot(a, s) : -1;
+    const PageTile<D> tile{lds};
+    const int lane_row = threadIdx.x / LPR, e = (threadIdx.x % LPR) * 8;
+    const uint16_t *src = IS_V ? n.v : n.k;
+    const int64_t stride = IS_V ? n.v_stride : n.k_stride;
+
+    auto row8 = [&](int p) -> u32x4 {  // position p's new row
+        const int row = sq.row0 + p - start;
+        const uint16_t *head = src + row * stride + h * D;
+        if (IS_V) return *(const u32x4 *)(head + e);
+        return normed_rotated<D>(head, e, n.k_norm, n, n.pos ? n.pos[row] : p);
+    };
+
+    if constexpr (BITS == 16) {
+        if (id < 0) return;
+        const int lo = max(lo_all, page << log2p), hi = min(hi_all, (page + 1) << log2p);
+        const int64_t at = kv_block_at(a, id, h);
+        for (int p = lo + lane_row; p < hi; p += RPP) {
+            const u32x4 v = row8(p);
+            if (IS_V) tile.put(p & (P - 1), e, v);
+            else *(u32x4 *)((uint16_t *)a.k + at + (p & (P - 1)) * D + e) = v;
+        }
+        if (IS_V) {
+            __syncthreads();
+            store_transposed<D>((uint16_t *)a.v + at, log2p, tile, lo & (P - 1), ((hi - 1) & (P - 1)) + 1);
+        }
+        return;
+    } else {
+        if (slot < 0) return;
+        uint16_t *tails = IS_V ? a.v_tail : a.k_tail;
+        // Older rows are read from the first page's half when it fills up.  A
+        // newer page of this call that keeps its rows in the same half must not
+        // overwrite them first, so the first page's workgroup stores those rows
+        // too, after it has read.
+        const bool first_reads = ((first + 1) << log2p) <= hi_all && lo_all > (first << log2p);
+        const int newer = last - ((last - first) & 1);
+        auto store_rows = [&](int pg) {  // the new rows of page pg: into the tile, and its open page
+            const int lo = max(lo_all, pg << log2p), hi = min(hi_all, (pg + 1) << log2p);
+            const int64_t at = kv_block_at(a, (int64_t)slot * 2 + (pg & 1), h);
+            uint32_t m = 0;
+            for (int p = lo + lane_row; p < hi; p += RPP) {
+                const u32x4 v = row8(p);
+                m = abs_bits_max(m, v);
+                tile.put(p & (P - 1), e, v);
+            }
+            return m;
+        };
+        auto keep_rows = [&](int pg) {  // from the tile into the open page
+            const int lo = max(lo_all, pg << log2p), hi = min(hi_all, (pg + 1) << log2p);
+            uint16_t *tail = tails + kv_block_at(a, (int64_t)slot * 2 + (pg & 1), h);
+            if (IS_V) {
+                store_transposed<D>(tail, log2p, tile, lo & (P - 1), ((hi - 1) & (P - 1)) + 1);
+            } else {
+                for (int p = lo + lane_row; p < hi; p += RPP)
+                    *(u32x4 *)(tail + (p & (P - 1)) * D + e) = tile.get(p & (P - 1), e);
+            }
+        };
+        const bool full = ((page + 1) << log2p) <= hi_all;
+        const bool reads = t == 0 && first_reads;
+        const bool keeps = page >= last - 1 && !(t > 0 && first_reads && page == newer);
+        if (!full && !keeps) return;
+        uint32_t m = store_rows(page);
+        if (reads) {  // the page's older rows
+            const uint16_t *tail = tails + kv_block_at(a, (int64_t)slot * 2 + (page & 1), h);
+            const int older = lo_all & (P - 1);
+            if (IS_V) {
+                const int nc = (older + 7) >> 3;
+                for (int i = threadIdx.x; i < nc * D; i += KVA_THREADS) {
+                    const int d = i / nc, c = i - d * nc;
+                    const u32x4 v = *(const u32x4 *)(tail + ((int64_t)d << log2p) + c * 8);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t b = (j & 1) ? v[j / 2] >> 16 : v[j / 2] & 0xFFFFu;
+                        if (c * 8 + j < older) {
+                            tile.t[(c * 8 + j) * tile.ROW + d] = (uint16_t)b;
+                            m = max(m, b & 0x7FFFu);
+                        }
+                    }
+                }
+            } else {
+                for (int r = lane_row; r < older; r += RPP) {
+                    const u32x4 v = *(const u32x4 *)(tail + r * D + e);
+                    m = abs_bits_max(m, v);
+                    tile.put(r, e, v);
+                }
+            }
+        }
+        if (full) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, WAVE));
+            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+        }
+        __syncthreads();
+        if (keeps) keep_rows(page);
+        if (full && id >= 0) {
+            m = max(max(red[0], red[1]), max(red[2], red[3]));
+            const float amax = bf16_to_f32((uint16_t)m);
+            // a page with an infinity or NaN has no codes: its scale is NaN
+            const float scale = m < 0x7F80u ? __fdiv_rn(amax, 127.0f) : NAN, inv = __frcp_rn(scale);
+            if (threadIdx.x == 0) (IS_V ? a.v_scale : a.k_scale)[(int64_t)id * a.kv_heads + h] = scale;
+            uint8_t *codes = (uint8_t *)(IS_V ? a.v : a.k) + kv_block_at(a, id, h);
+            // sixteen codes a store: a sixteenth of a row's D (k) or of a page's tokens (v)
+            for (int i = threadIdx.x; i < (P * D) / 16; i += KVA_THREADS) {
+                u32x4 out;
+                const int row = IS_V ? (i & ((P >> 4) - 1)) * 16 : i / (D / 16);
+                const int col = IS_V ? i >> (log2p - 4) : (i % (D / 16)) * 16;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int o = w * 4 + j;
+                        const float x = bf16_to_f32(IS_V ? tile.t[(row + o) * tile.ROW + col]
+                                                         : tile.t[row * tile.ROW + col + o]);
+                        word |= (amax == 0.0f ? 0u : qz_code(x, scale, inv, 127.0f) & 0xFFu) << (8 * j);
+                    }
+                    out[w] = word;
+                }
+                *(u32x4 *)(codes + (int64_t)i * 16) = out;
+            }
+        }
+        if (reads && newer > first) {  // the rows that share the half just read
+            __syncthreads();
+            store_rows(newer);
+            __syncthreads();
+            keep_rows(newer);
+        }
+    }
+}
+
+template <int D, int BITS>
+__global__ __launch_bounds__(KVA_THREADS) void k_kv_append(KvArgs a, KvAppend n, int touched, int page_groups,
+                                                           int q_groups)
+{
+    extern __shared__ __align__(16) uint16_t kva_tile[];
+    __shared__ uint32_t red[KVA_THREADS / WAVE];
+    int b = blockIdx.x;
+    if (b < page_groups) {
+        const int is_v = b & 1;
+        b >>= 1;
+        const int h = b % a.kv_heads;
+        b /= a.kv_heads;
+        const int t = b % touched, s = b / touched;
+        if (is_v) append_page<D, BITS, true>(a, n, s, t, h, kva_tile, red);
+        else append_page<D, BITS, false>(a, n, s, t, h, kva_tile, red);
+        return;
+    }
+    // queries: q_groups workgroups a sequence
+    b -= page_groups;
+    const int s = b / q_groups;
+    const KvSeq sq = kv_seq(a, s);
+    const int64_t i = (int64_t)(b % q_groups) * KVA_THREADS + threadIdx.x;
+    const int64_t head_row = i / (D / 8);
+    const int e = (int)(i % (D / 8)) * 8;
+    const int r = (int)(head_row / a.q_heads), h = (int)(head_row % a.q_heads);
+    if (r >= sq.n) return;  // the lanes of a row leave together
+    const int row = sq.row0 + r, p = sq.len - sq.n_pos + r;
+    const u32x4 v = normed_rotated<D>(n.q + row * n.q_stride + h * D, e, n.q_norm, n, n.pos ? n.pos[row] : p);
+    *(u32x4 *)(n.q_out + ((int64_t)row * a.q_heads + h) * D + e) = v;
+}
+
+// ---------------------------------------------------------------- read
+
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void read_page(const KvArgs &a, uint16_t *out, int s, int t, int h, uint16_t *lds)
+{
+    const KvSeq sq = kv_seq(a, s);
+    const int L = kv_limit(a, sq), start = sq.len - sq.n_pos, log2p = a.page_log2, P = 1 << log2p;
+    // the first touched page is the one of the first row with a position (rows before it read as 0)
+    const int first = max(start, 0) >> log2p, page = first + t;
+    const int lo = max(t == 0 ? start : (page << log2p), start), hi = min((page + 1) << log2p, start + sq.n);
+    if (hi <= lo) return;
+    const uint16_t *half = nullptr;
+    int64_t id = kv_page(a, s, page);
+    float scale = 1.0f;
+    if (BITS == 8) {
+        if (id >= 0 && ((page + 1) << log2p) > L) {  // still open
+            const int slot = kv_slot(a, s);
+            if (slot >= 0) half = (IS_V ? a.v_tail : a.k_tail) + kv_block_at(a, (int64_t)slot * 2 + (page & 1), h);
+            id = -1;
+        }
+        if (id >= 0) scale = (IS_V ? a.v_scale : a.k_scale)[id * a.kv_heads + h];
+    } else if (id >= 0) {
+        half = (const uint16_t *)(IS_V ? a.v : a.k) + kv_block_at(a, id, h);
+    }
+    const uint8_t *codes = BITS == 8 && id >= 0 ? (const uint8_t *)(IS_V ? a.v : a.k) + kv_block_at(a, id, h) : nullptr;
+    const PageTile<D> tile{lds};
+    auto decoded = [&](u32x2 w) {
+        u32x4 r;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const int32_t c = (int32_t)w[d];
+            r[2 * d] = to_bf16x2((float)((c << 24) >> 24) * scale, (float)((c << 16) >> 24) * scale);
+            r[2 * d + 1] = to_bf16x2((float)((c << 8) >> 24) * scale, (float)(c >> 24) * scale);
+        }
+        return r;
+    };
+    if (IS_V) {
+        // eight tokens of one d at a time into the tile
+        const int nc = P >> 3;
+        for (int i = threadIdx.x; i < nc * D; i += KVA_THREADS) {
+            const int d = i / nc, c = i - d * nc;
+            u32x4 v = {0, 0, 0, 0};
+            if (codes) v = decoded(*(const u32x2 *)(codes + ((int64_t)d << log2p) + c * 8));
+            else if (half) v = *(const u32x4 *)(half + ((int64_t)d << log2p) + c * 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                tile.t[(c * 8 + j) * tile.ROW + d] = (uint16_t)((j & 1) ? v[j / 2] >> 16 : v[j / 2]);
+        }
+        __syncthreads();
+    }
+    constexpr int LPR = D / 8, RPP = KVA_THREADS / LPR;
+    const int e = (threadIdx.x % LPR) * 8;
+    for (int p = lo + threadIdx.x / LPR; p < hi; p += RPP) {
+        u32x4 v = {0, 0, 0, 0};
+        if (p >= 0 && p < L) {
+            const int r = p & (P - 1);
+            if (IS_V) v = tile.get(r, e);
+            else if (codes) v = decoded(*(const u32x2 *)(codes + r * D + e));
+            else if (half) v = *(const u32x4 *)(half + r * D + e);
+        }
+        *(u32x4 *)(out + ((int64_t)(sq.row0 + p - start) * a.kv_heads + h) * D + e) = v;
+    }
+}
+
+template <int D, int BITS>
+__global__ __launch_bounds__(KVA_THREADS) void k_kv_read(KvArgs a, uint16_t *k, uint16_t *v, int touched)
+{
+    extern __shared__ __align__(16) uint16_t kva_tile[];
+    int b = blockIdx.x;
+    const int is_v = b & 1;
+    b >>= 1;
+    const int h = b % a.kv_heads;
+    b /= a.kv_heads;
+    const int t = b % touched, s = b / touched;
+    if (is_v) read_page<D, BITS, true>(a, v, s, t, h, kva_tile);
+    else read_page<D, BITS, false>(a, k, s, t, h, kva_tile);
+}
+
+// Pages that max_rows rows can touch, wherever they start.
+static int touched_pages(const KvArgs &a) { return ((a.max_rows - 2) >> a.page_log2) + 2; }
+
+template <int D>
+static size_t tile_bytes(const KvArgs &a) { return ((size_t)PageTile<D>::ROW << a.page_log2) * 2; }
+
+template <int D, int BITS>
+static hipError_t append(const KvArgs &a, const KvAppend &n, hipStream_t st)
+{
+    const int touched = touched_pages(a);
+    const int64_t pages = (int64_t)a.n_seq * touched * a.kv_heads * 2;
+    const int64_t q_groups = n.q ? ((int64_t)a.max_rows * a.q_heads * (D / 8) + KVA_THREADS - 1) / KVA_THREADS : 0;
+    if (pages + q_groups * a.n_seq > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_kv_append<D, BITS>), dim3((unsigned)(pages + q_groups * a.n_seq)), dim3(KVA_THREADS),
+                       tile_bytes<D>(a), st, a, n, touched, (int)pages, (int)q_groups);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const KvArgs &a, const KvAppend &n, hipStream_t st)
+{
+    if (a.head_dim == 64) return a.kv_bits == 8 ? append<64, 8>(a, n, st) : append<64, 16>(a, n, st);
+    return a.kv_bits == 8 ? append<128, 8>(a, n, st) : append<128, 16>(a, n, st);
+}
+
+template <int D, int BITS>
+static hipError_t read(const KvArgs &a, uint16_t *k, uint16_t *v, hipStream_t st)
+{
+    const int touched = touched_pages(a);
+    const int64_t pages = (int64_t)a.n_seq * touched * a.kv_heads * 2;
+    if (pages > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_kv_read<D, BITS>), dim3((unsigned)pages), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, k, v,
+                       touched);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvArgs &a, uint16_t *k, uint16_t *v, hipStream_t st)
+{
+    if (a.head_dim == 64) return a.kv_bits == 8 ? read<64, 8>(a, k, v, st) : read<64, 16>(a, k, v, st);
+    return a.kv_bits == 8 ? read<128, 8>(a, k, v, st) : read<128, 16>(a, k, v, st);
+}
+
+}  // namespace moe

@@ -108,4 +108,48 @@ hipError_t launch_combine(const void *y, const int32_t *inv, const float *topk_w
                           const uint16_t *res, void *out, int T, int H, int k, int out_f32, int y_f16, int y_by_pair,
                           hipStream_t st);
 
+// the paged key/value cache (kv_append.hip, kv_attention.hip); the fields are
+// those of moe_kv_shape, moe_kv_batch, moe_kv_cache and moe_kv_rotary
+struct KvArgs {
+    int n_seq, rows, max_rows, max_len;
+    int q_heads, kv_heads, head_dim, kv_bits;
+    int page_log2, n_pages, max_pages, n_slots;
+    int window, causal;
+    float scale;
+    const int32_t *row_start, *kv_len, *pages, *slots;
+    void *k, *v;
+    float *k_scale, *v_scale;
+    uint16_t *k_tail, *v_tail;
+};
+struct KvAppend {
+    const uint16_t *k, *v, *q;
+    int64_t k_stride, v_stride, q_stride;
+    uint16_t *q_out;
+    const float *cos, *sin, *q_norm, *k_norm;
+    const int32_t *pos;
+    int n_pos, rot_dim, pairs;
+    float eps;
+};
+hipError_t launch_kv_append(const KvArgs &a, const KvAppend &n, hipStream_t st);
+hipError_t launch_kv_read(const KvArgs &a, uint16_t *k, uint16_t *v, hipStream_t st);
+size_t kv_attention_workspace(const KvArgs &a);
+hipError_t launch_kv_attention(const KvArgs &a, const uint16_t *q, int64_t q_stride, void *out, int out_f32,
+                               float *lse, void *ws, hipStream_t st);
+
+// few-token products with packed int4 weights and group scales (linear_q4.hip)
+struct LinearQ4 {
+    int T, N, K, group;
+    const uint16_t *x;
+    int64_t x_stride;
+    const uint8_t *q;
+    const void *scales;
+    int scales_bf16;
+    const uint16_t *residual;
+    void *out;
+    int out_f32;
+    void *ws;
+};
+size_t linear_q4_workspace(int T, int N, int K);
+hipError_t launch_linear_q4(const LinearQ4 &a, hipStream_t st);
+
 }  // namespace moe

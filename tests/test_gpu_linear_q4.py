@@ -1,0 +1,163 @@
+"""moe_linear_q4 against the product in 64 bits.
+
+Tolerance: products of bf16 activations and int4 codes are exact in f32, every sum runs in f32: K terms give at most
+K * 2^-24 of the terms' magnitudes in the worst order; pairwise or tiled orders stay far below, K / 8 is allowed. A bf16
+output is the f32 one rounded once."""
+import numpy as np
+import pytest
+
+import int4_routed_expert_02_amd as moe
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    moe.load()
+
+
+def make(T, N, K, group, bf16_scales, seed=0, pad=0, std=1.0):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = (torch.randn(T, K + pad, generator=g, device="cuda") * std).to(torch.bfloat16)[:, :K]
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)   # every code, -8 too
+    s = torch.rand(N, K // group, generator=g, device="cuda") * 0.02 - 0.005
+    return x, q, s.to(torch.bfloat16) if bf16_scales else s
+
+
+def exact(x, q, s, group):
+    b = q.cpu().numpy().astype(np.int64)
+    c = np.empty((b.shape[0], b.shape[1] * 2), np.int64)
+    c[:, 0::2], c[:, 1::2] = b & 15, b >> 4
+    c = np.where(c > 7, c - 16, c)
+    w = c * np.repeat(s.double().cpu().numpy(), group, axis=1)
+    xd = x.double().cpu().numpy()
+    return xd @ w.T, np.abs(xd) @ np.abs(w).T
+
+
+def run(x, q, s, residual=None, f32=True, out=None):
+    import torch
+    T, N, K = x.shape[0], q.shape[0], x.shape[1]
+    if out is None:
+        out = torch.full((T, N), 99.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    ws = torch.full((moe.moe_linear_q4_workspace_bytes(T, N, K),), 255, dtype=torch.uint8, device="cuda")
+    moe.moe_linear_q4(x, q, s, out, residual, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(T, N, K, group, bf16_scales, pad=0, tag="", std=1.0):
+    import torch
+    x, q, s = make(T, N, K, group, bf16_scales, pad=pad, std=std)
+    ref, mag = exact(x, q, s, group)
+    # the unpack's offset (the codes are held as code + 136) leaves f32 sums up to 136 / 4 times the terms'
+    tol = mag * (K / 8 * 2.0 ** -24 + 40 * 2.0 ** -22)
+    out = run(x, q, s)
+    err = np.abs(out.double().cpu().numpy() - ref) / tol
+    say(f"linear T={T} N={N} K={K} g={group} {'bf16' if bf16_scales else 'f32'} {tag}: {err.max():.3f} of the bound")
+    assert (err <= 1).all()
+    assert torch.equal(out, run(x, q, s))
+    half = run(x, q, s, f32=False)
+    assert torch.equal(half, out.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("bf16_scales", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 8, 15, 16, 17, 32, 33, 64])
+def test_tokens(T, group, bf16_scales):
+    check(T, 96, 512, group, bf16_scales, pad=8 if T % 2 else 0)
+
+
+@pytest.mark.parametrize("N", [1, 15, 16, 17, 63, 65, 257, 1000])
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_odd_widths(N, T):
+    check(T, N, 384, 32, True)
+    check(T, N, 384, 128, False)
+
+
+@pytest.mark.parametrize("group,K", [(32, 32), (32, 96), (64, 64), (64, 192), (128, 128), (32, 992), (64, 1984), (128, 1152),
+                                     (32, 4128), (128, 8192), (64, 5184), (32, 16384)])
+@pytest.mark.parametrize("T", [1, 4, 20])
+def test_depths(T, group, K):
+    check(T, 48, K, group, False)
+    check(T, 33, K, group, True)
+
+
+@pytest.mark.parametrize("T", [65, 100, 129])
+def test_larger_batches(T):
+    check(T, 80, 512, 64, False)
+
+
+def test_wide():
+    check(1, 20001, 256, 32, False)
+    check(32, 5000, 1024, 128, True)
+
+
+def test_residual_and_in_place():
+    import torch
+    for T in (1, 7, 32, 70):
+        x, q, s = make(T, 130, 256, 32, False)
+        r = torch.randn(T, 130, device="cuda").to(torch.bfloat16)
+        plain = run(x, q, s)
+        want = plain + r.float()
+        assert torch.equal(run(x, q, s, r), want)
+        got = r.clone()
+        run(x, q, s, got, out=got)
+        assert torch.equal(got, want.to(torch.bfloat16))
+
+
+def test_large_and_special_activations():
+    """Activations beyond f16's range; an infinity or NaN stays in its own token's row."""
+    import torch
+    check(5, 64, 512, 64, False, std=1e6, tag="large")
+    check(5, 64, 512, 64, False, std=1e-12, tag="small")
+    for T in (2, 20):
+        x, q, s = make(T, 64, 512, 64, False)
+        clean = run(x, q, s)
+        x = x.clone()
+        x[1, 77] = float("nan")
+        bad = run(x, q, s)
+        assert torch.isnan(bad[1]).all()
+        keep = [t for t in range(T) if t != 1]
+        assert torch.equal(bad[keep], clean[keep])
+
+
+def test_quantiser_feeds_it():
+    """Weights that moe_quantize_rows cut into groups: the product of the dequantised weights."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    w = torch.randn(200, 512, generator=g, device="cuda") * 0.05
+    codes, scales = moe.moe_quantize_rows(w.view(-1, 64), 4)
+    x = torch.randn(6, 512, generator=g, device="cuda").to(torch.bfloat16)
+    out = run(x, codes.view(200, 256), scales.view(200, 8))
+    ref, mag = exact(x, codes.view(200, 256), scales.view(200, 8), 64)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= mag * 2e-5).all()
+    full = x.double().cpu().numpy() @ w.double().cpu().numpy().T
+    assert np.linalg.norm(ref - full) < 0.2 * np.linalg.norm(full)
+
+
+def test_graph_replays():
+    import torch
+    x, q, s = make(3, 300, 1024, 64, False)
+    out = torch.empty(3, 300, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.moe_linear_q4_workspace_bytes(3, 300, 1024), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        moe.moe_linear_q4(x, q, s, out, None, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        moe.moe_linear_q4(x, q, s, out, None, ws)
+    for f in (1.0, 0.5, 4.0):
+        x.mul_(f)
+        want = run(x, q, s, f32=False)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

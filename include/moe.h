@@ -528,8 +528,8 @@ int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batch, const mo
  *   out = sum_j exp(z_j - m) v_j / l,  lse = m + log l.
  * A row that sees nothing gets out 0 and lse -infinity.  Products run on the matrix
  * cores with f32 accumulation: q, keys and int8 codes are exact in bf16, and each weight
- * exp(z_j - m) is rounded to 16 bits for the product with the values (2^-8 relative or
- * better) while l, m and all sums stay in f32.  Positions from kv_len on are never used;
+ * exp(z_j - m) enters the product with the values as the sum of two bf16 values (2^-16
+ * relative) while l, m and all sums stay in f32.  Positions from kv_len on are never used;
  * a value that is infinite or NaN at a position some row of the call sees may
  * reach other rows of the same sequence and head.
  *   q    [rows][q_heads][head_dim] bf16, row stride q_row_stride (moe_kv_append's q_out)

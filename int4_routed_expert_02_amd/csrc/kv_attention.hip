@@ -13,12 +13,12 @@
 // in 16-byte pieces of 16 consecutive positions, which lie in one page whatever
 // its size, with one pair of scales.
 //
-// An int8 code is exact in bf16 and in f16.  Scores: q and the codes in bf16,
-// the page's scale times log2(e) * scale after the product.  Values: codes in
-// f16, and the weight times the page's scale relative to the largest seen (a
-// power of two), rounded to f16 (2^-11 relative; f16 keeps what is within 2^-24
-// of the largest, the rest cannot be seen in a 32-bit sum either).  bf16 pages
-// and open pages: weights rounded to bf16 (2^-8), so that values keep their range.
+// An int8 code is exact in bf16, so codes, keys and queries enter the products as
+// they are; a page's key scale (times log2(e) * scale) is applied to its scores in
+// f32 and its value scale to its weights.  A weight enters the second product as
+// the sum of two bf16 values, 2^-16 relative at any distance from the maximum.
+// One bf16 value (2^-8) makes an output's error half as large again as its own
+// rounding, and f16 loses weights far below the maximum.
 #include "kv_device.h"
 
 namespace moe {
@@ -26,8 +26,8 @@ namespace moe {
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr float M_NONE = -1e30f;  // running maximum before any score
 // The running maximum is raised only when a score passes it by more than this
-// (in powers of two): weights stay below 2^8, far inside f16, and most tiles skip
-// the reduction over lanes and the rescaling of the accumulator.
+// (in powers of two): weights stay below 2^8, and most tiles skip the reduction
+// over lanes and the rescaling of the accumulator.
 constexpr float M_SLACK = 8.0f;
 
 struct KvAttend {
@@ -35,7 +35,7 @@ struct KvAttend {
     int64_t q_stride;
     void *out;
     float *lse;
-    float *part;  // partial results: [ns][rows][q_heads] of (D accumulators), then the same of (m, l)
+    float *part;  // partial results: [ns][rows][q_heads] of (D accumulators), then the same of (m, sum)
     int out_f32, ns, group;
 };
 
@@ -47,18 +47,18 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, r);
 }
 
-// Two weights to f16, rounded toward zero (one instruction; below 2^-10
-// relative, while a rounding to nearest takes three).
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
+// Two weights as hi + lo in bf16: hi the upper halves as they are (truncated),
+// lo the rest rounded; together 2^-16 relative.
+__device__ __forceinline__ void split_bf16x2(float e0, float e1, uint32_t &hi, uint32_t &lo)
 {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+    hi = __builtin_amdgcn_perm(__float_as_uint(e1), __float_as_uint(e0), 0x07060302u);
+    lo = cvt_bf16x2(e0 - __uint_as_float(__float_as_uint(e0) & 0xFFFF0000u),
+                    e1 - __uint_as_float(__float_as_uint(e1) & 0xFFFF0000u));
 }
 
-// Eight int8 codes to exact f16: code + 1152 by byte permutes, then the packed subtraction.
-__device__ __forceinline__ u32x4 codes_f16(u32x2 w)
+__device__ __forceinline__ float uniform(float v)
 {
-    const f16x8 v = __builtin_bit_cast(f16x8, unpack_int8x8_f16(w)) - (_Float16)INT8_F16_BIAS;
-    return __builtin_bit_cast(u32x4, v);
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
@@ -69,14 +69,6 @@ __device__ __forceinline__ void kv_sees(const KvArgs &a, const KvSeq &sq, int L,
     const int p = sq.len - sq.n_pos + i;
     hi = a.causal ? min(max(p + 1, 0), L) : L;
     lo = a.window ? max(0, p - a.window + 1) : 0;
-}
-
-// The smallest power of two that is not below v (2^-100 at least).
-__device__ __forceinline__ float pow2_above(float v)
-{
-    uint32_t u = __float_as_uint(v);
-    u = min((u & 0x7F800000u) + ((u & 0x7FFFFFu) ? 0x800000u : 0u), 253u << 23);
-    return __uint_as_float(max(u, 27u << 23));
 }
 
 // ---------------------------------------------------------------- few rows
@@ -114,11 +106,10 @@ __device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, 
 // + 16 n and, of a tile, the positions 16 g .. 16 g + 15 with g = lane / 16.
 template <int D, int NT>
 struct DecState {
-    f32x4 o[NT][D / 16];  // o[n][dt][i]: value d = 16 dt + 4 g + i of the lane's row n, over vref
+    f32x4 o[NT][D / 16];  // o[n][dt][i]: value d = 16 dt + 4 g + i of the lane's row n
     float m[NT], l[NT];   // maximum (the same in a row's four lanes), this lane's share of the sum
-    float vref, ivref;    // power of two the accumulator's values are relative to, and its inverse
 
-    __device__ void clear(float v)
+    __device__ void clear()
     {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -127,27 +118,15 @@ struct DecState {
             m[n] = M_NONE;
             l[n] = 0.f;
         }
-        vref = v;
-        ivref = 1.0f / v;
     }
 
-    // New largest scores xm (this lane's) and, in 8 bits, its page's value scale.
-    __device__ __forceinline__ void raise(const float (&xm)[NT], float vs)
+    // xm: this lane's new largest scores
+    __device__ __forceinline__ void raise(const float (&xm)[NT])
     {
-        bool up = vs > vref;
+        bool up = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) up |= xm[n] > m[n] + M_SLACK;
         if (!__builtin_amdgcn_ballot_w64(up)) return;
-        float v = vs == vs ? vs : 0.f;
-        v = fmaxf(v, __shfl_xor(v, 16, WAVE));
-        v = fmaxf(v, __shfl_xor(v, 32, WAVE));
-        float fv = 1.0f;
-        if (v > vref) {
-            const float r = pow2_above(v);
-            fv = vref / r;
-            vref = r;
-            ivref = __uint_as_float((254u << 23) - __float_as_uint(r));
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x = xm[n];
@@ -156,9 +135,8 @@ struct DecState {
             const float mn = fmaxf(m[n], x), f = __builtin_amdgcn_exp2f(m[n] - mn);
             m[n] = mn;
             l[n] *= f;
-            const float fo = f * fv;
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) o[n][t] *= fo;
+            for (int t = 0; t < D / 16; ++t) o[n][t] *= f;
         }
     }
 };
@@ -205,11 +183,12 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
     kv_sees(a, sq, L, 0, x0, hi_all);
 
     DecState<D, NT> st;
-    st.clear(BITS == 8 ? 0x1p-100f : 1.0f);
+    st.clear();
 
-    // scores of a tile -> weights in the second product's operand order
-    auto softmax = [&](f32x4 (&z)[NT][4], float c, float vs, int b0, bool full, bool valid, uint32_t (&p)[NT][8],
-                       bool f16) {
+    // Scores of a tile -> weights in the second product's operand order, as the
+    // sum of two bf16 values (2^-16 relative): the matrix cores have time for the
+    // second product here, where the cache's bytes are what is waited for.
+    auto softmax = [&](f32x4 (&z)[NT][4], float c, float vs, int b0, bool full, bool valid, uint32_t (&p)[NT][2][8]) {
         const int j0 = b0 + 16 * g;
         float xm[NT];
         if (full) {
@@ -232,21 +211,35 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
                 }
             }
         }
-        st.raise(xm, vs);
-        const float w = vs * st.ivref, cc = full ? c : 1.0f;
+        st.raise(xm);
+        const float cc = full ? c : 1.0f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float e[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i / 4][i % 4], cc, -st.m[n]));
-                st.l[n] += e[i];
-                e[i] *= w;
-                if (!full) e[i] = z[n][i / 4][i % 4] == -INFINITY ? 0.f : e[i];  // 0 * NaN scale
+            for (int i = 0; i < 16; i += 2) {
+                float e[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float zz = z[n][i / 4][i % 4 + j];
+                    e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(zz, cc, -st.m[n]));
+                    st.l[n] += e[j];
+                    if (BITS == 8) e[j] *= vs;
+                    if (!full) e[j] = zz == -INFINITY ? 0.f : e[j];  // 0 * NaN scale
+                }
+                split_bf16x2(e[0], e[1], p[n][0][i / 2], p[n][1][i / 2]);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[n][i] = f16 ? cvt_f16x2(e[2 * i], e[2 * i + 1]) : cvt_bf16x2(e[2 * i], e[2 * i + 1]);
         }
+    };
+    // o += V^T P^T for one d tile: vb the 64 positions' values in two steps
+    auto values = [&](int d, const u32x4 (&vb)[2], const uint32_t (&p)[NT][2][8]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                    st.o[n][d] = mfma_bf16(vb[k], u32x4{p[n][w][4 * k], p[n][w][4 * k + 1], p[n][w][4 * k + 2],
+                                                        p[n][w][4 * k + 3]}, st.o[n][d]);
     };
     // operand row r16 of step u is position 16 kchunk + 4 u + krow of the tile
     const int krow = r16 & 3, kchunk = r16 >> 2;
@@ -305,18 +298,12 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
                 const int b0 = tl.t0 + 64 * tile;
                 const bool valid = idg >= 0;
                 const bool full = b0 >= lo_all && b0 + 64 <= min(hi_all, tl.F) && !__builtin_amdgcn_ballot_w64(!valid);
-                uint32_t p[NT][8];
-                softmax(z, valid ? ks * zscale : 0.f, valid ? vs : 0.f, b0, full, valid, p, true);
+                uint32_t p[NT][2][8];
+                softmax(z, valid ? ks * zscale : 0.f, valid ? vs : 0.f, b0, full, valid, p);
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const u32x4 vb = codes_f16(k ? u32x2{vq[d][2], vq[d][3]} : u32x2{vq[d][0], vq[d][1]});
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            st.o[n][d] = mfma_f16(vb, u32x4{p[n][4 * k], p[n][4 * k + 1], p[n][4 * k + 2], p[n][4 * k + 3]},
-                                                  st.o[n][d]);
-                    }
+                    const u32x4 vb[2] = {unpack_int8x8(u32x2{vq[d][0], vq[d][1]}), unpack_int8x8(u32x2{vq[d][2], vq[d][3]})};
+                    values(d, vb, p);
                 }
                 if (!more) break;
                 idg = idg1;
@@ -390,16 +377,10 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
                     for (int d = 0; d < DT; ++d) vb[d][k][w] &= keep;
                 }
         }
-        uint32_t p[NT][8];
-        softmax(z, zscale, valid ? 1.0f : 0.f, b0, full, valid, p, false);
+        uint32_t p[NT][2][8];
+        softmax(z, zscale, 1.0f, b0, full, valid, p);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    st.o[n][d] = mfma_bf16(vb[d][k], u32x4{p[n][4 * k], p[n][4 * k + 1], p[n][4 * k + 2], p[n][4 * k + 3]},
-                                           st.o[n][d]);
+        for (int d = 0; d < DT; ++d) values(d, vb[d], p);
     }
 
     // ---- the waves' results together: maxima and sums first, then the accumulators pairwise
@@ -424,7 +405,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
         for (int w = 0; w < DEC_WAVES; ++w)
             l_all[n] += sl[w * 16 * NT + 16 * n + r16] *
                         __builtin_amdgcn_exp2f(sm[w * 16 * NT + 16 * n + r16] - m_all[n]);
-        const float f = __builtin_amdgcn_exp2f(st.m[n] - m_all[n]) * st.vref;
+        const float f = __builtin_amdgcn_exp2f(st.m[n] - m_all[n]);
 #pragma unroll
         for (int d = 0; d < DT; ++d) st.o[n][d] *= f;
     }
@@ -472,20 +453,393 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
     }
 }
 
+// ---------------------------------------------------------------- many rows
+
+constexpr int TILE_WAVES = 4, TILE_ROWS = 32 * TILE_WAVES;  // query rows of a workgroup, 32 a wave
+
+constexpr int TILE_MIN = 8;                                 // tiles of 64 positions in a part, at least
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32_bf16(u32x4 a, u32x4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+// The tiles that the query rows [128 rt, 128 rt + 128) of a sequence and head
+// look at, and how they are cut into parts.
+struct RowTile {
+    int lo, hi;         // positions some row sees lie in [lo, hi)
+    int t0, total;      // first tile's position, tiles
+    int parts, per;
+};
+
+__device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, int group, int rt, int ns)
+{
+    const int i0 = rt * TILE_ROWS / group, i1 = min((rt * TILE_ROWS + TILE_ROWS - 1) / group, sq.n - 1);
+    RowTile t;
+    int x;
+    kv_sees(a, sq, L, i0, t.lo, x);
+    kv_sees(a, sq, L, i1, x, t.hi);
+    t.t0 = t.lo & ~63;
+    t.total = t.hi > t.t0 ? (t.hi - t.t0 + 63) >> 6 : 0;
+    t.parts = max(1, min(ns, (t.total + TILE_MIN - 1) / TILE_MIN));
+    t.per = (t.total + t.parts - 1) / t.parts;
+    return t;
+}
+
+// Tiles of 64 positions in LDS, two of them (one is filled while the other is used):
+//   K  [64 rows][D] bf16, position t of the tile in row t with bits 2 and 3 of t exchanged, so
+//      that a lane's 16 scores of a 32 x 32 product belong to runs of 8 consecutive positions,
+//      which is what the second product takes from a lane; 16-byte units of a row XORed with
+//      the row, so that the 32 rows of an operand read lie on different banks;
+//   V  [D rows][64 positions] bf16, 16-byte units XORed with the row;
+//   per chunk of 16 positions: score scale, value scale (negative where the chunk is absent), its
+//   log2 and inverse.
+template <int D>
+struct TileLds {
+    static constexpr int KB = 64 * D * 2, BYTES = 2 * KB + 64;
+    char *base;
+    __device__ u32x4 *k(int buf, int row, int unit) const
+    {
+        return (u32x4 *)(base + buf * BYTES + row * D * 2 + ((unit ^ (row & 7)) << 4));
+    }
+    __device__ u32x4 *v(int buf, int d, int unit) const
+    {
+        return (u32x4 *)(base + buf * BYTES + KB + d * 128 + ((unit ^ (d & 7)) << 4));
+    }
+    __device__ float *chunk(int buf, int c) const { return (float *)(base + buf * BYTES + 2 * KB) + c * 4; }
+};
+
+template <int D, int BITS>
+__global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles)
+{
+    constexpr int QS = D / 16, DT = D / 32;     // contraction steps of a score, d tiles
+    constexpr int NR = D / 64 * (BITS / 8);     // 16-byte pieces of K (and of V) a thread stages
+    extern __shared__ __align__(16) char tile_lds[];
+    const TileLds<D> lds{tile_lds};
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h32 = lane >> 5, c32 = lane & 31;
+    // kv head fastest (a head's workgroups share an L2), the last rows (the longest, if causal) first
+    int b = blockIdx.x;
+    const int kh = b % a.kv_heads;
+    b /= a.kv_heads;
+    const int split = b % t.ns;
+    b /= t.ns;
+    const int s = b % a.n_seq, rt = row_tiles - 1 - b / a.n_seq;
+    const KvSeq sq = kv_seq(a, s);
+    const int rows = sq.n * t.group;
+    if (rt * TILE_ROWS >= rows) return;
+    const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
+    const RowTile tl = row_tile(a, sq, L, t.group, rt, t.ns);
+    if (split >= tl.parts) return;
+    const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
+    const int F = BITS == 8 ? (L >> log2p) << log2p : 0;  // from here on: the open page
+    const int slot = BITS == 8 ? kv_slot(a, s) : -1;
+
+    // the wave's rows, the lane's row
+    const int r0 = rt * TILE_ROWS + wave * 32, r = min(r0 + c32, rows - 1);
+    const int i = r / t.group, head = kh * t.group + r % t.group;
+    int lo, hi, lo_all, hi_all, x;
+    kv_sees(a, sq, L, i, lo, hi);
+    kv_sees(a, sq, L, min(r0, rows - 1) / t.group, x, hi_all);
+    int lo_min = x, hi_max;
+    kv_sees(a, sq, L, min(r0 + 31, rows - 1) / t.group, lo_all, hi_max);
+    u32x4 q[QS];
+    {
+        const uint16_t *src = t.q + (sq.row0 + i) * t.q_stride + head * D + 8 * h32;
+#pragma unroll
+        for (int k = 0; k < QS; ++k) q[k] = *(const u32x4 *)(src + 16 * k);
+        if (a.scale < 0.f) {
+#pragma unroll
+            for (int k = 0; k < QS; ++k) q[k] ^= 0x80008000u;
+        }
+    }
+    const float zscale = fabsf(a.scale) * LOG2E;
+
+    f32x16 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] = 0.f;
+    float m = M_NONE, l = 0.f;
+
+    // ---- staging: thread tid has position tid / 4 of a tile's K (a quarter of its values) and, of V,
+    // rows d = tid / 4 (+ 64) and chunk tid % 4
+    const int kt = tid >> 2, kq = tid & 3, vd = tid >> 2, vc = tid & 3;
+    u32x4 kr[NR], vr[NR];
+    float ks = 0.f, vs = 0.f;  // this lane's chunk (tid % 4)
+    int idk = -1, idv = -1;    // pages of the K position and of the V chunk of the tile to load next
+    auto page_of = [&](int tile, int chunk) {
+        const int j = tl.t0 + 64 * tile + 16 * chunk;
+        return j < L ? kv_page(a, s, j >> log2p) : -1;
+    };
+    auto ids_of = [&](int tile) {
+        idk = page_of(tile, kt >> 4);
+        idv = page_of(tile, vc);
+    };
+    const int64_t page_elems = ((int64_t)a.kv_heads * D) << log2p, head_at = (int64_t)kh * D << log2p;
+    constexpr int EB = BITS / 8;
+    auto load = [&](int tile) {
+        const int jk = tl.t0 + 64 * tile + kt, jv = tl.t0 + 64 * tile + 16 * vc;
+        const char *sk = (const char *)a.k + (max(idk, 0) * page_elems + head_at + (jk & (P - 1)) * D + kq * (D / 4)) * EB;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) kr[n] = *(const u32x4 *)(sk + 16 * n);
+        const char *sv = (const char *)a.v + (max(idv, 0) * page_elems + head_at + (vd << log2p) + (jv & (P - 1))) * EB;
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+#pragma unroll
+            for (int u = 0; u < EB; ++u) vr[n * EB + u] = *(const u32x4 *)(sv + ((int64_t)(64 * n) << log2p) * EB + 16 * u);
+        if (BITS == 8) {
+            ks = idv >= 0 ? a.k_scale[(int64_t)idv * a.kv_heads + kh] : 0.f;
+            vs = idv >= 0 ? a.v_scale[(int64_t)idv * a.kv_heads + kh] : 0.f;
+        }
+    };
+    const int krow = (kt & 0x33) | ((kt & 4) << 1) | ((kt & 8) >> 1);
+    auto put_chunk = [&](int buf, bool valid, float c, float v) {
+        if (tid < 4) *(f32x4 *)lds.chunk(buf, tid) = f32x4{c, valid ? v : -1.0f, __log2f(v), __builtin_amdgcn_rcpf(v)};
+    };
+    // Eight bf16 values from position j on, 0 in the place of those no row here
+    // sees: these may hold anything, and 0 * NaN is not 0.
+    auto seen = [&](u32x4 v, int j) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int jj = j + 2 * w;
+            v[w] &= (jj >= tl.lo && jj < tl.hi ? 0xFFFFu : 0u) | (jj + 1 >= tl.lo && jj + 1 < tl.hi ? 0xFFFF0000u : 0u);
+        }
+        return v;
+    };
+    auto put = [&](int buf, int tile) {
+        if (BITS == 16) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) *lds.k(buf, krow, kq * NR + n) = kr[n];
+            const int j = tl.t0 + 64 * tile + 16 * vc;
+            const bool whole = idv >= 0 && j >= tl.lo && j + 16 <= tl.hi;
+#pragma unroll
+            for (int n = 0; n < D / 64; ++n)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    *lds.v(buf, vd + 64 * n, 2 * vc + u) = whole ? vr[n * 2 + u]
+                                                           : idv < 0 ? u32x4{0, 0, 0, 0} : seen(vr[n * 2 + u], j + 8 * u);
+            put_chunk(buf, idv >= 0, zscale, 1.0f);
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                *lds.k(buf, krow, 2 * (kq * (D / 64) + n) + u) = unpack_int8x8(u32x2{kr[n][2 * u], kr[n][2 * u + 1]});
+                *lds.v(buf, vd + 64 * n, 2 * vc + u) = unpack_int8x8(u32x2{vr[n][2 * u], vr[n][2 * u + 1]});
+            }
+        put_chunk(buf, idv >= 0, ks * zscale, vs);
+    };
+    // a tile with chunks of the open page, loaded where it is needed
+    auto put_open = [&](int buf, int tile) {
+        const int b0 = tl.t0 + 64 * tile, jk = b0 + kt, jv = b0 + 16 * vc;
+        const bool openk = jk >= F, openv = jv >= F;
+        if (idk >= 0 && openk && slot >= 0) {
+            const uint16_t *src = a.k_tail + kv_block_at(a, (int64_t)slot * 2 + ((jk >> log2p) & 1), kh) + (jk & (P - 1)) * D;
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n) *lds.k(buf, krow, kq * (D / 32) + n) = *(const u32x4 *)(src + kq * (D / 4) + 8 * n);
+        } else {
+            const char *src = (const char *)a.k + idk * page_elems + head_at + (jk & (P - 1)) * D + kq * (D / 4);
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+                *lds.k(buf, krow, kq * (D / 32) + n) =
+                    idk >= 0 && !openk ? unpack_int8x8(*(const u32x2 *)(src + 8 * n)) : u32x4{0, 0, 0, 0};
+        }
+        const bool valid = idv >= 0 && (!openv || slot >= 0);
+        float cks = 1.f, cvs = 1.f;
+        if (valid && !openv) {
+            cks = a.k_scale[(int64_t)idv * a.kv_heads + kh];
+            cvs = a.v_scale[(int64_t)idv * a.kv_heads + kh];
+        }
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = ((vd + 64 * n) << log2p) + (jv & (P - 1)) + 8 * u;
+                u32x4 v = {0, 0, 0, 0};
+                if (valid && openv)
+                    v = seen(*(const u32x4 *)(a.v_tail + kv_block_at(a, (int64_t)slot * 2 + ((jv >> log2p) & 1), kh) + at),
+                             jv + 8 * u);
+                else if (valid)
+                    v = unpack_int8x8(*(const u32x2 *)((const char *)a.v + idv * page_elems + head_at + at));
+                *lds.v(buf, vd + 64 * n, 2 * vc + u) = v;
+            }
+        put_chunk(buf, valid, cks * zscale, cvs);
+    };
+    // ---- one tile: scores, weights, values
+    auto step = [&](int buf, int tile) {
+        const int b0 = tl.t0 + 64 * tile;
+        if (b0 >= hi_max || b0 + 64 <= lo_min) return;  // nothing for this wave
+        f32x16 z[2];
+#pragma unroll
+        for (int T = 0; T < 2; ++T) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[T][j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < QS; ++k) z[T] = mfma32_bf16(*lds.k(buf, 32 * T + c32, 2 * k + h32), q[k], z[T]);
+        }
+        // z[n / 2][8 (n % 2) + j]: chunk n, position b0 + 16 n + 8 h32 + j
+        float c[4], vs[4], lv[4], iv[4];
+        bool all = true;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 ch = *(const f32x4 *)lds.chunk(buf, n);
+            c[n] = BITS == 8 ? uniform(ch[0]) : zscale;
+            vs[n] = uniform(ch[1]);
+            lv[n] = BITS == 8 ? uniform(ch[2]) : 0.f;
+            iv[n] = BITS == 8 ? uniform(ch[3]) : 1.f;
+            all &= vs[n] >= 0x1p-60f && vs[n] <= 0x1p60f;
+        }
+        float xm = -INFINITY;
+        auto raise = [&]() {
+            if (!__builtin_amdgcn_ballot_w64(xm > m + M_SLACK)) return;
+            xm = fmaxf(xm, __shfl_xor(xm, 32, WAVE));
+            const float mn = fmaxf(m, xm), f = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= f;
+        };
+        auto values = [&](int n, const float (&e)[8]) {
+            u32x4 p[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hi_, lo_;
+                split_bf16x2(e[2 * j], e[2 * j + 1], hi_, lo_);
+                p[0][j] = hi_;
+                p[1][j] = lo_;
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const u32x4 vb = *lds.v(buf, 32 * d + c32, 2 * n + h32);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) o[d] = mfma32_bf16(vb, p[w], o[d]);
+            }
+        };
+        if (all && b0 >= lo_all && b0 + 64 <= hi_all) {
+            // every row sees every position: the value scale goes into the exponent, and a chunk's
+            // sum is divided by it once
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float mx = z[n >> 1][(n & 1) * 8];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) mx = fmaxf(mx, z[n >> 1][(n & 1) * 8 + j]);
+                xm = fmaxf(xm, mx * c[n]);
+            }
+            raise();
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float sub = lv[n] - m;
+                float e[8], sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n >> 1][(n & 1) * 8 + j], c[n], sub));
+                    sum += e[j];
+                }
+                l = __builtin_fmaf(sum, iv[n], l);
+                values(n, e);
+            }
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const bool valid = !(vs[n] < 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int pos = b0 + 16 * n + 8 * h32 + j;
+                const bool see = valid && pos >= lo && pos < hi;
+                const float v = see ? z[n >> 1][(n & 1) * 8 + j] * c[n] : -INFINITY;
+                z[n >> 1][(n & 1) * 8 + j] = v;
+                xm = fmaxf(xm, v);
+            }
+        }
+        raise();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = z[n >> 1][(n & 1) * 8 + j];
+                e[j] = __builtin_amdgcn_exp2f(v - m);
+                l += e[j];
+                e[j] = v == -INFINITY ? 0.f : e[j] * vs[n];  // 0 * NaN scale
+            }
+            values(n, e);
+        }
+    };
+
+    // tiles without an open page: the next one's loads fly while one is used
+    const int closed = BITS == 8 ? min(end, max(begin, (F - tl.t0) >> 6)) : end;
+    if (begin < closed) {
+        ids_of(begin);
+        load(begin);
+        put(begin & 1, begin);
+        if (begin + 1 < closed) ids_of(begin + 1);
+        __syncthreads();
+        for (int tile = begin; tile < closed; ++tile) {
+            const bool more = tile + 1 < closed;
+            if (more) load(tile + 1);
+            step(tile & 1, tile);
+            if (more) {
+                put((tile + 1) & 1, tile + 1);
+                if (tile + 2 < closed) ids_of(tile + 2);
+            }
+            __syncthreads();
+        }
+    }
+    if (BITS == 8) {
+        for (int tile = closed; tile < end; ++tile) {
+            ids_of(tile);
+            put_open(0, tile);
+            __syncthreads();
+            step(0, tile);
+            __syncthreads();
+        }
+    }
+
+    l += __shfl_xor(l, 32, WAVE);
+    if (r0 + c32 >= rows) return;
+    const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + head;
+    const bool whole = tl.parts == 1;
+    const int64_t pt = (int64_t)split * a.rows * a.q_heads + at;
+    const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = 32 * d + 8 * j + 4 * h32;
+            const f32x4 v = f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]} * f;
+            if (!whole) *(f32x4 *)(t.part + pt * D + e) = v;
+            else if (t.out_f32) *(f32x4 *)((float *)t.out + at * D + e) = v;
+            else *(u32x2 *)((uint16_t *)t.out + at * D + e) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+        }
+    if (h32) return;
+    if (!whole) {
+        float *ml = t.part + (int64_t)t.ns * a.rows * a.q_heads * D + pt * 2;
+        ml[0] = m;
+        ml[1] = l;
+    } else if (t.lse) {
+        t.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * (1.0f / LOG2E);
+    }
+}
+
 // The parts of a sequence's rows together, in order.  D / 4 lanes a row and head.
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int groups)
+__global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int groups, int few)
 {
     const int s = blockIdx.x / groups;
     const KvSeq sq = kv_seq(a, s);
     const int L = kv_limit(a, sq);
-    if (sq.n == 0) return;
-    const int parts = dec_tiles(a, sq, L, t.ns).parts;
-    if (parts == 1) return;
     const int64_t idx = (int64_t)(blockIdx.x % groups) * 256 + threadIdx.x;
     const int64_t rh = idx / (D / 4);
     const int i = (int)(rh / a.q_heads), h = (int)(rh % a.q_heads), d = (int)(idx % (D / 4)) * 4;
     if (i >= sq.n) return;
+    const int parts = few ? dec_tiles(a, sq, L, t.ns).parts
+                          : row_tile(a, sq, L, t.group, (i * t.group + h % t.group) / TILE_ROWS, t.ns).parts;
+    if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;
     float m = M_NONE;
@@ -501,96 +855,6 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     if (t.out_f32) *(f32x4 *)((float *)t.out + at * D + d) = o;
     else *(u32x2 *)((uint16_t *)t.out + at * D + d) = u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
     if (t.lse && d == 0) t.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * (1.0f / LOG2E);
-}
-
-template <int D, int BITS>
-__global__ __launch_bounds__(256) void k_attn_row(KvArgs a, const uint16_t *q, int64_t q_stride, void *out,
-                                                  int out_f32, float *lse)
-{
-    __shared__ float qs[D], w[256], red[4], acc4[256];
-    const int tid = threadIdx.x, h = blockIdx.y, i = blockIdx.x % a.max_rows, s = blockIdx.x / a.max_rows;
-    const KvSeq sq = kv_seq(a, s);
-    if (i >= sq.n) return;
-    const int row = sq.row0 + i, p = sq.len - sq.n_pos + i, L = kv_limit(a, sq), P = 1 << a.page_log2;
-    const int kh = h / (a.q_heads / a.kv_heads);
-    const int hi = a.causal ? min(L, p + 1) : L, lo = a.window ? max(0, p - a.window + 1) : 0;
-    const int slot = BITS == 8 ? kv_slot(a, s) : -1;
-    if (tid < D) qs[tid] = bf16_to_f32(q[row * q_stride + h * D + tid]) * a.scale;
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, acc = 0.f;  // acc: value tid % D over a share of the positions
-    constexpr int SH = 256 / D;
-    auto block_of = [&](int j, const uint16_t *&half, const uint16_t *&vhalf, int64_t &id) {
-        const int pg = j >> a.page_log2;
-        id = kv_page(a, s, pg);
-        half = vhalf = nullptr;
-        if (id < 0) return false;
-        if (BITS == 16) {
-            half = (const uint16_t *)a.k + kv_block_at(a, id, kh);
-            vhalf = (const uint16_t *)a.v + kv_block_at(a, id, kh);
-        } else if (((pg + 1) << a.page_log2) > L) {
-            if (slot < 0) return false;
-            const int64_t at = kv_block_at(a, (int64_t)slot * 2 + (pg & 1), kh);
-            half = a.k_tail + at;
-            vhalf = a.v_tail + at;
-        }
-        return true;
-    };
-    for (int c = lo; c < hi; c += 256) {
-        const int j = c + tid;
-        float z = -INFINITY;
-        const uint16_t *half, *vhalf;
-        int64_t id;
-        if (j < hi && block_of(j, half, vhalf, id)) {
-            z = 0.f;
-            const int r = j & (P - 1);
-            if (half) {
-                for (int d = 0; d < D; ++d) z += qs[d] * bf16_to_f32(half[r * D + d]);
-            } else {
-                const int8_t *kc = (const int8_t *)a.k + kv_block_at(a, id, kh) + r * D;
-                for (int d = 0; d < D; ++d) z += qs[d] * (float)kc[d];
-                z *= a.k_scale[id * a.kv_heads + kh];
-            }
-        }
-        float mx = z;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, WAVE));
-        if ((tid & 63) == 0) red[tid >> 6] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float base = mn > -INFINITY ? mn : 0.f;
-        const float e = z > -INFINITY || z != z ? __expf(z - base) : 0.f, f = m > -INFINITY ? __expf(m - base) : 0.f;
-        w[tid] = e;
-        __syncthreads();
-        float sum = e;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, WAVE);
-        if ((tid & 63) == 0) red[tid >> 6] = sum;
-        acc *= f;
-        const int d = tid % D;
-        for (int t = tid / D; t < 256 && c + t < hi; t += SH) {
-            if (w[t] == 0.f || !block_of(c + t, half, vhalf, id)) continue;
-            const int r = (c + t) & (P - 1);
-            if (half) acc += w[t] * bf16_to_f32(vhalf[d * P + r]);
-            else
-                acc += w[t] * (float)((const int8_t *)a.v)[kv_block_at(a, id, kh) + d * P + r] *
-                       a.v_scale[id * a.kv_heads + kh];
-        }
-        __syncthreads();
-        l = l * f + red[0] + red[1] + red[2] + red[3];
-        m = mn;
-        __syncthreads();
-    }
-    acc4[tid] = acc;
-    __syncthreads();
-    if (tid < D) {
-        float o = 0.f;
-        for (int t = 0; t < SH; ++t) o += acc4[tid + t * D];
-        o = l > 0.f || l != l ? o / l : 0.f;
-        const int64_t at = ((int64_t)row * a.q_heads + h) * D + tid;
-        if (out_f32) ((float *)out)[at] = o;
-        else ((__bf16 *)out)[at] = (__bf16)o;
-        if (lse && tid == 0) lse[(int64_t)row * a.q_heads + h] = l > 0.f || l != l ? m + __logf(l) : -INFINITY;
-    }
 }
 
 
@@ -610,10 +874,31 @@ static int dec_parts(const KvArgs &a)
     return (int)(ns < 1 ? 1 : ns);
 }
 
+static int64_t row_tiles_of(const KvArgs &a)
+{
+    return ((int64_t)a.max_rows * (a.q_heads / a.kv_heads) + TILE_ROWS - 1) / TILE_ROWS;
+}
+
+constexpr int TILE_TARGET = 512;  // workgroups of the many-row kernel that fill the chip
+
+static int tile_parts(const KvArgs &a)
+{
+    int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
+    const int64_t most = (len / 64 + TILE_MIN) / TILE_MIN, base = (int64_t)a.n_seq * a.kv_heads * row_tiles_of(a);
+    int64_t ns = base > 0 ? TILE_TARGET / base : 1;
+    if (ns > most) ns = most;
+    return (int)(ns < 1 ? 1 : ns);
+}
+
+constexpr int FEW_ROWS = 32;  // rows of a key/value head that the few-row kernel holds
+
+static bool few_rows(const KvArgs &a) { return (int64_t)a.max_rows * (a.q_heads / a.kv_heads) <= FEW_ROWS; }
+
+static int parts_of(const KvArgs &a) { return few_rows(a) ? dec_parts(a) : tile_parts(a); }
+
 size_t kv_attention_workspace(const KvArgs &a)
 {
-    if ((int64_t)a.max_rows * (a.q_heads / a.kv_heads) > 32) return 256;
-    const int ns = dec_parts(a);
+    const int ns = parts_of(a);
     return ns > 1 ? (size_t)ns * a.rows * a.q_heads * (a.head_dim + 2) * 4 : 256;
 }
 
@@ -628,20 +913,33 @@ static hipError_t attend_few(const KvArgs &a, const KvAttend &t, hipStream_t st)
 }
 
 template <int D, int BITS>
+static hipError_t attend_many(const KvArgs &a, const KvAttend &t, unsigned grid, int tiles, hipStream_t st)
+{
+    constexpr size_t lds = 2 * TileLds<D>::BYTES;
+    // more LDS than a kernel gets unasked
+    static const hipError_t attr = hipFuncSetAttribute((const void *)k_attn_tile<D, BITS>,
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (attr != hipSuccess) return attr;
+    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3(grid), dim3(TILE_WAVES * WAVE), lds, st, a, t, tiles);
+    return hipGetLastError();
+}
+
+template <int D, int BITS>
 static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
     const int64_t rows = (int64_t)a.max_rows * t.group;
-    if (rows > 32) {
-        const int64_t gx = (int64_t)a.n_seq * a.max_rows;
-        if (gx > INT32_MAX / 256 || a.q_heads > 65535) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((k_attn_row<D, BITS>), dim3((unsigned)gx, a.q_heads), dim3(256), 0, st, a, t.q, t.q_stride,
-                           t.out, t.out_f32, t.lse);
-        return hipGetLastError();
+    hipError_t e;
+    if (few_rows(a)) {
+        e = rows <= 16 ? attend_few<D, BITS, 1>(a, t, st) : attend_few<D, BITS, 2>(a, t, st);
+    } else {
+        const int64_t tiles = row_tiles_of(a), grid = tiles * a.n_seq * a.kv_heads * t.ns;
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        e = attend_many<D, BITS>(a, t, (unsigned)grid, (int)tiles, st);
     }
-    const hipError_t e = rows <= 16 ? attend_few<D, BITS, 1>(a, t, st) : attend_few<D, BITS, 2>(a, t, st);
     if (e != hipSuccess || t.ns == 1) return e;
     const int64_t groups = ((int64_t)a.max_rows * a.q_heads * (D / 4) + 255) / 256;
-    hipLaunchKernelGGL((k_attn_parts<D>), dim3((unsigned)(groups * a.n_seq)), dim3(256), 0, st, a, t, (int)groups);
+    hipLaunchKernelGGL((k_attn_parts<D>), dim3((unsigned)(groups * a.n_seq)), dim3(256), 0, st, a, t, (int)groups,
+                       few_rows(a) ? 1 : 0);
     return hipGetLastError();
 }
 
@@ -657,7 +955,7 @@ hipError_t launch_kv_attention(const KvArgs &args, const uint16_t *q, int64_t q_
     t.out_f32 = out_f32;
     t.lse = lse;
     t.part = (float *)ws;
-    t.ns = dec_parts(args);
+    t.ns = parts_of(args);
     t.group = a.q_heads / a.kv_heads;
     if (a.head_dim == 64) return a.kv_bits == 8 ? attend<64, 8>(a, t, st) : attend<64, 16>(a, t, st);
     return a.kv_bits == 8 ? attend<128, 8>(a, t, st) : attend<128, 16>(a, t, st);

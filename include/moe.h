@@ -570,7 +570,7 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  * group is 32, 64 or 128 and divides K; any N and T (made for T <= 64: a larger batch
  * reads the weights again for every 64 tokens).
  * Errors: MOE_ERR_SHAPE (negative sizes, K % group, a format or stride out of range),
- * MOE_ERR_UNSUPPORTED (group), MOE_ERR_NULL, MOE_ERR_ALIGN (x, q, scales, ws; residual and
+ * MOE_ERR_UNSUPPORTED (group, K above 2^26, x_row_stride above 2^25), MOE_ERR_NULL, MOE_ERR_ALIGN (x, q, scales, ws; residual and
  * out to their elements; x_row_stride % 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or
  * N == 0 is a no-op.
  */

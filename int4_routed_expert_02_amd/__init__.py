@@ -196,10 +196,26 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+_torch = _current = None  # torch, once a call has needed it, and the current stream's handle as torch keeps it
+
+
+def _bind_torch():
+    """torch is imported by the first call that needs it, not with the package."""
+    global _torch, _current
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    _torch = torch
+    get_device, raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    # a tenth of a microsecond; torch.cuda.current_stream() builds an object, 3 us
+    _current = lambda: raw_stream(get_device())  # noqa: E731
+    return torch
+
+
+def _stream(stream) -> Optional[int]:
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is None:
+        _bind_torch()
+    return _current()
 
 
 def moe_validate_shape(sh: MoeShape) -> int:
@@ -390,11 +406,11 @@ def kv_rotary(cos=None, sin=None, rot_dim=0, pos=None, q_norm=None, k_norm=None,
 
 def _head_rows(t, rows, heads, dim, what):
     """Pointer and row stride of a [rows][heads][dim] bf16 tensor whose rows may be apart."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    torch = _torch or _bind_torch()
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{what} must be a bfloat16 GPU tensor")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != rows or shape[1] != heads or shape[2] != dim:
+    stride = t.stride()
+    if t.shape != (rows, heads, dim):
         raise ValueError(f"{what} must be [{rows}][{heads}][{dim}]")
     if rows and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
@@ -402,8 +418,8 @@ def _head_rows(t, rows, heads, dim, what):
 
 
 def _head_out(t, rows, heads, dim, what, f32=False):
-    import torch
-    if t.dtype != (torch.float32 if f32 else torch.bfloat16) or tuple(t.shape) != (rows, heads, dim):
+    torch = _torch or _bind_torch()
+    if t.dtype is not (torch.float32 if f32 else torch.bfloat16) or t.shape != (rows, heads, dim):
         raise ValueError(f"{what} must be a {'float32' if f32 else 'bfloat16'} [{rows}][{heads}][{dim}] tensor")
     return _ptr(t)
 
@@ -432,7 +448,7 @@ def moe_kv_append(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, ro
 def moe_kv_attention(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, q, out, lse=None, ws=None, stream=None):
     """Attention of the batch's rows over the cache (include/moe.h): out [rows][q_heads][head_dim] (bf16, or f32 with
     MOE_OUT_F32), lse [rows][q_heads] f32 or None, ws moe_kv_workspace_bytes(sh) bytes."""
-    import torch
+    torch = _torch or _bind_torch()
     _kv_fits(sh, batch, cache)
     qp, qs = _head_rows(q, sh.rows, sh.q_heads, sh.head_dim, "q")
     op = _head_out(out, sh.rows, sh.q_heads, sh.head_dim, "out", bool(sh.flags & MOE_OUT_F32))
@@ -457,25 +473,23 @@ def moe_linear_q4_workspace_bytes(T: int, N: int, K: int) -> int:
 def moe_linear_q4(x, q, scales, out, residual=None, ws=None, stream=None):
     """out = x W^T (+ residual) for a few tokens, W packed int4 with group scales (include/moe.h): x [T][K] bf16 (rows
     possibly apart), q uint8 [N][K/2], scales f32 or bf16 [N][K/group], out [T][N] bf16 or f32."""
-    import torch
-    T, K = x.shape
-    N = q.shape[0]
-    if x.dtype != torch.bfloat16 or not x.is_cuda or (x.numel() and x.stride(1) != 1):
+    torch = _torch or _bind_torch()
+    (T, K), N, f32, bf16 = x.shape, q.shape[0], torch.float32, torch.bfloat16
+    stride, groups = x.stride(), scales.shape[1]
+    if x.dtype is not bf16 or not x.is_cuda or (stride[1] != 1 and T and K > 1):
         raise ValueError("x must be a bfloat16 GPU tensor with contiguous rows")
-    if tuple(q.shape) != (N, K // 2) or q.dtype not in (torch.uint8, torch.int8):
+    if q.shape != (N, K // 2) or q.dtype not in (torch.uint8, torch.int8):
         raise ValueError("q must be [N][K/2] bytes")
-    if scales.dim() != 2 or scales.shape[0] != N or scales.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("scales must be [N][K/group] float32 or bfloat16")
-    if tuple(out.shape) != (T, N) or out.dtype not in (torch.float32, torch.bfloat16):
+    if scales.shape != (N, groups) or scales.dtype not in (f32, bf16) or groups == 0 or K % groups:
+        raise ValueError("scales must be [N][K/group] float32 or bfloat16, group dividing K")
+    if out.shape != (T, N) or out.dtype not in (f32, bf16):
         raise ValueError("out must be [T][N] float32 or bfloat16")
-    if residual is not None and (tuple(residual.shape) != (T, N) or residual.dtype != torch.bfloat16):
+    if residual is not None and (residual.shape != (T, N) or residual.dtype is not bf16):
         raise ValueError("residual must be a bfloat16 [T][N] tensor")
-    if scales.shape[1] == 0 or K % scales.shape[1]:
-        raise ValueError("scales must be [N][K/group] with group dividing K")
-    _check(load().moe_linear_q4(T, N, K, K // scales.shape[1], x.data_ptr(), x.stride(0) if T > 1 else K, _ptr(q),
-                                _ptr(scales), MOE_SRC_F32 if scales.dtype == torch.float32 else MOE_SRC_BF16,
-                                _ptr(residual), _ptr(out), MOE_OUT_F32 if out.dtype == torch.float32 else 0, _ptr(ws),
-                                ws.numel() if ws is not None else 0, _stream(stream)), "moe_linear_q4")
+    _check(load().moe_linear_q4(T, N, K, K // groups, x.data_ptr(), stride[0] if T > 1 else K, _ptr(q), _ptr(scales),
+                                MOE_SRC_F32 if scales.dtype is f32 else MOE_SRC_BF16, _ptr(residual), _ptr(out),
+                                MOE_OUT_F32 if out.dtype is f32 else 0, _ptr(ws), ws.numel() if ws is not None else 0,
+                                _stream(stream)), "moe_linear_q4")
 
 
 class KvPages:

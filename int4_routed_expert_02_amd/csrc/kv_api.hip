@@ -190,6 +190,7 @@ extern "C" int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, con
     if (scale_format != MOE_SRC_F32 && scale_format != MOE_SRC_BF16) return MOE_ERR_SHAPE;
     if ((int64_t)T * N > ((int64_t)1 << 40)) return MOE_ERR_SHAPE;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
+    if (K > 1 << 26 || x_row_stride > 1 << 25) return MOE_ERR_UNSUPPORTED;  // 32-bit offsets inside a workgroup
     if (T == 0 || N == 0) return MOE_OK;
     if (!x || !q || !scales || !out) return MOE_ERR_NULL;
     if (!aligned(x, 16) || x_row_stride % 8 || !aligned(q, 16) || !aligned(scales, 16)) return MOE_ERR_ALIGN;

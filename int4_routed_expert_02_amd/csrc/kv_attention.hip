@@ -916,10 +916,9 @@ template <int D, int BITS>
 static hipError_t attend_many(const KvArgs &a, const KvAttend &t, unsigned grid, int tiles, hipStream_t st)
 {
     constexpr size_t lds = 2 * TileLds<D>::BYTES;
-    // more LDS than a kernel gets unasked
-    static const hipError_t attr = hipFuncSetAttribute((const void *)k_attn_tile<D, BITS>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (attr != hipSuccess) return attr;
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = lds > 64 << 10 ? allow_lds((const void *)k_attn_tile<D, BITS>, (int)lds, done) : hipSuccess;
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3(grid), dim3(TILE_WAVES * WAVE), lds, st, a, t, tiles);
     return hipGetLastError();
 }

@@ -16,15 +16,14 @@
 // the offset comes out with -1.5 * sum x of the group, taken by one product
 // against a constant whose result is where the group's accumulators start.  The
 // scale (times 16) joins a group's sum in f32.
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_launch.h"
 
 namespace moe {
 
 constexpr int LQ_BLOCK = 128;  // k of one step: a 16-byte piece for each of a column's four lanes
-// Waves of a workgroup: sixteen where 128 registers do, else eight.
-constexpr int lq_max_waves(int rt, int tt) { return rt * tt <= 2 ? 16 : 8; }
-
 // Eight nibbles -> eight bf16 of (code + 24) / 16, in the order of unpack_int4x8.
 __device__ __forceinline__ u32x4 lq_unpack(uint32_t w)
 {
@@ -46,56 +45,104 @@ __device__ __forceinline__ u32x4 lq_transpose(u32x4 v)
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// RT tiles of 16 columns, TT of 16 tokens a wave; the workgroup's waves share K.
-template <int GROUP, bool SB, int RT, int TT>
-__global__ __launch_bounds__(lq_max_waves(RT, TT) * WAVE) void k_linear_q4(LinearQ4 a, int t0)
+// A load that touches 16 rows costs the memory pipeline as much for 4 bytes a row
+// as for 64, about 64 cycles, so only the codes come straight into their lanes.  A
+// wave's activations (TR rows of a block of 128 k) and scales come in runs
+// along k and go through a piece of LDS of its own: no barriers, so the
+// waves drift apart and one loads while another computes.
+template <int GROUP, int RT, int TR, int WAVES>
+struct LqLds {
+    static constexpr int GB = LQ_BLOCK / GROUP, TT = (TR + 15) / 16;
+    static constexpr int XROW = LQ_BLOCK * 2 + 16;                               // bytes of a token's row
+    static constexpr int X_BYTES = TR * XROW, WAVE_BYTES = X_BYTES + 16 * RT * GB * 4;
+    static constexpr int R_BYTES = WAVES * RT * TT * 1024;                       // the waves' sums, in the same place at the end
+    static constexpr int BYTES = WAVES * WAVE_BYTES > R_BYTES ? WAVES * WAVE_BYTES : R_BYTES;
+};
+
+// GB scales from an address of their own alignment
+template <bool SB, int GB>
+__device__ __forceinline__ void lq_scales(const char *p, float (&s)[GB])
 {
-    constexpr int GB = LQ_BLOCK / GROUP;  // groups of a block
-    extern __shared__ __align__(16) float lq_red[];  // [waves][RT][TT][64 lanes][4]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int g = lane >> 4, c16 = lane & 15;
-    const int tokens = min(a.T - t0 - (int)blockIdx.y * 16 * TT, 16 * TT), tok0 = t0 + blockIdx.y * 16 * TT;
-    const int n0 = blockIdx.x * 16 * RT, blocks = (a.K + LQ_BLOCK - 1) / LQ_BLOCK;
-    const int per = (blocks + waves - 1) / waves, b0 = wave * per, b1 = min(blocks, b0 + per);
-    const int groups = a.K / GROUP;
-
-    const uint8_t *wp[RT];
-    int64_t sp[RT];
-    const uint16_t *xp[TT];
+    if constexpr (SB) {
+        typedef uint16_t v_t __attribute__((ext_vector_type(GB), aligned(2)));
+        const v_t v = *(const v_t *)p;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int64_t n = min(n0 + 16 * r + c16, a.N - 1);
-        wp[r] = a.q + n * (a.K / 2);
-        sp[r] = n * groups;
+        for (int i = 0; i < GB; ++i) s[i] = bf16_to_f32(v[i]);
+    } else {
+        typedef float v_t __attribute__((ext_vector_type(GB), aligned(4)));
+        const v_t v = *(const v_t *)p;
+#pragma unroll
+        for (int i = 0; i < GB; ++i) s[i] = v[i];
     }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) xp[t] = a.x + (int64_t)(tok0 + min(16 * t + c16, tokens - 1)) * a.x_stride + 8 * g;
+}
 
-    u32x4 w[RT], x[TT][4];
-    float s[RT][GB];
-    auto load = [&](int b) {
-        const int k0 = b * LQ_BLOCK;
-        // the last block of a K that is no multiple of 128 ends early: its missing pieces are read
-        // from its first one and not used
-        const int piece = k0 + 32 * g < a.K ? 16 * g : 0;
+// 16 * RT columns, up to TR tokens; the workgroup's waves take the blocks of K in turn.
+template <int GROUP, bool SB, int RT, int TR, int WAVES>
+__global__ __launch_bounds__(WAVES *WAVE) void k_linear_q4(LinearQ4 a, int t0)
+{
+    using Lds = LqLds<GROUP, RT, TR, WAVES>;
+    constexpr int TT = Lds::TT, GB = Lds::GB, THREADS = WAVES * WAVE, XU = TR / 4, SS = SB ? 2 : 4;
+    extern __shared__ __align__(16) char lq_lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = lane >> 4, c16 = lane & 15;
+    const int tok0 = t0 + blockIdx.y * TR, tokens = min(a.T - tok0, TR);
+    const int n0 = blockIdx.x * 16 * RT, groups = a.K / GROUP, cols = min(16 * RT, a.N - n0);
+    const int blocks = (a.K + LQ_BLOCK - 1) / LQ_BLOCK;
+
+    // Offsets of the lane's loads from the workgroup's first row: rows past an edge are some row that
+    // is there, and their results are dropped.
+    uint32_t wo[RT], xo[XU];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            w[r] = *(const u32x4 *)(wp[r] + k0 / 2 + piece);
+    for (int r = 0; r < RT; ++r) wo[r] = (uint32_t)min(16 * r + c16, cols - 1) * (uint32_t)(a.K / 2) + 16 * g;
+#pragma unroll
+    for (int i = 0; i < XU; ++i) xo[i] = (uint32_t)min(g + 4 * i, tokens - 1) * (uint32_t)(a.x_stride * 2) + 16 * c16;
+    const uint32_t so = (uint32_t)min(lane & (16 * RT - 1), cols - 1) * (uint32_t)(groups * SS);
+    const char *wbase = (const char *)a.q + (int64_t)n0 * (a.K / 2);
+    const char *xbase = (const char *)(a.x + (int64_t)tok0 * a.x_stride);
+    const char *sbase = (const char *)a.scales + (int64_t)n0 * groups * SS;
+
+    u32x4 w[RT], x[XU];
+    float s[GB];
+    auto load = [&](int b) {
+        const char *wt = wbase + b * (LQ_BLOCK / 2), *xt = xbase + b * (LQ_BLOCK * 2), *st = sbase + b * (GB * SS);
+        if ((b + 1) * LQ_BLOCK <= a.K) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) w[r] = *(const u32x4 *)(wt + wo[r]);
+#pragma unroll
+            for (int i = 0; i < XU; ++i)
+                if (4 * i < tokens) x[i] = *(const u32x4 *)(xt + xo[i]);
+            lq_scales<SB, GB>(st + so, s);
+        } else {
+            // the last block ends early: activations and scales are 0 from K on, the codes there are the
+            // block's first ones (its first 32 are always there)
+            const int left = a.K - b * LQ_BLOCK;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) w[r] = *(const u32x4 *)(wt + (32 * g < left ? wo[r] : wo[r] - 16 * g));
+#pragma unroll
+            for (int i = 0; i < XU; ++i) {
+                x[i] = *(const u32x4 *)(xt + (8 * c16 < left ? xo[i] : xo[i] - 16 * c16));
+                if (8 * c16 >= left) x[i] = u32x4{0, 0, 0, 0};
+            }
 #pragma unroll
             for (int i = 0; i < GB; ++i) {
-                const int64_t at = sp[r] + min(b * GB + i, groups - 1);
-                s[r][i] = SB ? bf16_to_f32(((const uint16_t *)a.scales)[at]) : ((const float *)a.scales)[at];
+                float v[1];
+                lq_scales<SB, 1>(st + so + (i * GROUP < left ? i * SS : 0), v);
+                s[i] = i * GROUP < left ? v[0] : 0.f;
             }
         }
     };
-    auto load_x = [&](int b) {
+    char *const mine = lq_lds + wave * Lds::WAVE_BYTES;
+    char *const xput = mine + g * Lds::XROW + 16 * c16;
+    float *const sc = (float *)(mine + Lds::X_BYTES);
+    auto put = [&]() {
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int i = 0; i < XU; ++i)
+            if (4 * i < tokens) *(u32x4 *)(xput + 4 * i * Lds::XROW) = interleave_bf16x8(x[i]);
+        if (lane < 16 * RT) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[t][j] = *(const u32x4 *)(xp[t] + min(b * LQ_BLOCK + 32 * j, a.K - 32));
+            for (int i = 0; i < GB; ++i) sc[lane * GB + i] = s[i] * 16.0f;
+        }
     };
-    // the next block's activations are loaded ahead too where the registers are there
-    constexpr bool AHEAD = TT <= 2;
 
     f32x4 y[RT][TT];
 #pragma unroll
@@ -103,71 +150,69 @@ __global__ __launch_bounds__(lq_max_waves(RT, TT) * WAVE) void k_linear_q4(Linea
 #pragma unroll
         for (int t = 0; t < TT; ++t) y[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const u32x4 offset = {0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u};  // -1.5
-    if (b0 < b1) {
-        load(b0);
-        if (AHEAD) load_x(b0);
-    }
-    for (int b = b0; b < b1; ++b) {
-        if (!AHEAD) load_x(b);
-        u32x4 wb[RT], xb[TT][4];
-        float sb[RT][GB];
+    const char *xget[TT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            wb[r] = lq_transpose(w[r]);
+    for (int t = 0; t < TT; ++t) xget[t] = mine + min(16 * t + c16, tokens - 1) * Lds::XROW + 16 * g;
+
+    if (wave < blocks) load(wave);
+    for (int b = wave; b < blocks; b += WAVES) {
+        put();
+        // the wave's own writes, read by its other lanes: LDS keeps their order, the compiler is told to
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u32x4 wb[RT];
 #pragma unroll
-            for (int i = 0; i < GB; ++i) sb[r][i] = s[r][i] * 16.0f;
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) xb[t][j] = interleave_bf16x8(x[t][j]);
-        const int steps = min(4, (a.K - b * LQ_BLOCK) / 32);
-        if (b + 1 < b1) {
-            load(b + 1);
-            if (AHEAD) load_x(b + 1);
-        }
+        for (int r = 0; r < RT; ++r) wb[r] = lq_transpose(w[r]);
+        if (b + WAVES < blocks) load(b + WAVES);
 #pragma unroll
         for (int i = 0; i < GB; ++i) {
-            f32x4 acc[RT][TT];
-            if (i * (GROUP / 32) >= steps) break;
+            f32x4 acc[RT][TT], off[TT];
+            u32x4 xb[TT][GROUP / 32];
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+                off[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = i * (GROUP / 32); j < (i + 1) * (GROUP / 32); ++j) c = mfma_bf16(xb[t][j], offset, c);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][t] = c;
+                for (int j = 0; j < GROUP / 32; ++j) {
+                    xb[t][j] = *(const u32x4 *)(xget[t] + (i * (GROUP / 32) + j) * 64);
+                    off[t] = mfma_bf16(xb[t][j], offset, off[t]);
+                }
             }
 #pragma unroll
-            for (int j = i * (GROUP / 32); j < (i + 1) * (GROUP / 32); ++j)
+            for (int j = 0; j < GROUP / 32; ++j)
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const u32x4 v = lq_unpack(wb[r][j]);
+                    const u32x4 v = lq_unpack(wb[r][i * (GROUP / 32) + j]);
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[r][t] = mfma_bf16(xb[t][j], v, acc[r][t]);
+                    for (int t = 0; t < TT; ++t) acc[r][t] = mfma_bf16(xb[t][j], v, j ? acc[r][t] : off[t]);
                 }
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r) {
+                const float sv = sc[(16 * r + c16) * GB + i];
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[r][t][e] = __builtin_fmaf(sb[r][i], acc[r][t][e], y[r][t][e]);
+                    for (int e = 0; e < 4; ++e) y[r][t][e] = __builtin_fmaf(sv, acc[r][t][e], y[r][t][e]);
+            }
         }
     }
 
+    __syncthreads();
+    float *red = (float *)lq_lds;  // [waves][RT][TT][64 lanes][4]
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) *(f32x4 *)(lq_red + (((wave * RT + r) * TT + t) * 64 + lane) * 4) = y[r][t];
+        for (int t = 0; t < TT; ++t) *(f32x4 *)(red + (((wave * RT + r) * TT + t) * 64 + lane) * 4) = y[r][t];
     __syncthreads();
     // one value a thread and turn: column n, token t
-    for (int i = threadIdx.x; i < RT * TT * 256; i += blockDim.x) {
+    for (int i = tid; i < RT * TT * 256; i += THREADS) {
         const int c = i & 15, t16 = (i >> 4) & 15, t = (i >> 8) % TT, r = (i >> 8) / TT;
         const int n = n0 + 16 * r + c, tok = 16 * t + t16;
         if (n >= a.N || tok >= tokens) continue;
-        const float *src = lq_red + ((r * TT + t) * 64 + (t16 >> 2) * 16 + c) * 4 + (t16 & 3);
+        const float *src = red + ((r * TT + t) * 64 + (t16 >> 2) * 16 + c) * 4 + (t16 & 3);
         float v = 0.f;
-        for (int u = 0; u < waves; ++u) v += src[u * RT * TT * 256];
+#pragma unroll
+        for (int u = 0; u < WAVES; ++u) v += src[u * RT * TT * 256];
         const int64_t at = (int64_t)(tok0 + tok) * a.N + n;
         if (a.residual) v += bf16_to_f32(a.residual[at]);
         if (a.out_f32) ((float *)a.out)[at] = v;
@@ -177,14 +222,20 @@ __global__ __launch_bounds__(lq_max_waves(RT, TT) * WAVE) void k_linear_q4(Linea
 
 size_t linear_q4_workspace(int, int, int) { return 256; }
 
-template <int GROUP, bool SB, int RT, int TT>
-static hipError_t linear(const LinearQ4 &a, int waves, hipStream_t st)
+template <int GROUP, bool SB, int RT, int TR, int WAVES>
+static hipError_t linear(const LinearQ4 &a, hipStream_t st)
 {
+    constexpr int lds = LqLds<GROUP, RT, TR, WAVES>::BYTES;
+    if (lds > 64 << 10) {
+        static std::atomic<uint64_t> done{0};
+        const hipError_t e = allow_lds((const void *)k_linear_q4<GROUP, SB, RT, TR, WAVES>, lds, done);
+        if (e != hipSuccess) return e;
+    }
     const unsigned gx = (a.N + 16 * RT - 1) / (16 * RT);
-    for (int t0 = 0; t0 < a.T; t0 += 32768 * 16 * TT) {
-        const int64_t left = ((int64_t)a.T - t0 + 16 * TT - 1) / (16 * TT);
-        hipLaunchKernelGGL((k_linear_q4<GROUP, SB, RT, TT>), dim3(gx, (unsigned)(left < 32768 ? left : 32768)),
-                           dim3(waves * WAVE), waves * RT * TT * 1024, st, a, t0);
+    for (int64_t t0 = 0; t0 < a.T; t0 += 32768 * TR) {
+        const int64_t left = (a.T - t0 + TR - 1) / TR;
+        hipLaunchKernelGGL((k_linear_q4<GROUP, SB, RT, TR, WAVES>), dim3(gx, (unsigned)(left < 32768 ? left : 32768)),
+                           dim3(WAVES * WAVE), lds, st, a, (int)t0);
     }
     return hipGetLastError();
 }
@@ -192,19 +243,16 @@ static hipError_t linear(const LinearQ4 &a, int waves, hipStream_t st)
 template <int GROUP, bool SB>
 static hipError_t linear_tiles(const LinearQ4 &a, hipStream_t st)
 {
-    const int tiles = (a.N + 15) / 16, blocks = (a.K + LQ_BLOCK - 1) / LQ_BLOCK;
-    const int tt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-    const int rt = tiles >= 512 || (tt >= 2 && tiles >= 256) ? 2 : 1;
-    int waves = lq_max_waves(rt, tt);
-    while (waves > 4 && (waves > blocks || tiles / rt * waves > 256 * 32)) waves /= 2;
-    if (rt == 1) {
-        if (tt == 1) return linear<GROUP, SB, 1, 1>(a, waves, st);
-        if (tt == 2) return linear<GROUP, SB, 1, 2>(a, waves, st);
-        return linear<GROUP, SB, 1, 4>(a, waves, st);
-    }
-    if (tt == 1) return linear<GROUP, SB, 2, 1>(a, waves, st);
-    if (tt == 2) return linear<GROUP, SB, 2, 2>(a, waves, st);
-    return linear<GROUP, SB, 2, 4>(a, waves, st);
+    // Two tiles of columns a workgroup where they still fill the chip, else one: measured at 32 x 6144 x
+    // 8192 16 us against 25, at 1 x 1536 x 1024 (96 tiles) the other way round.  Sixteen waves for a few
+    // tokens of a long K and few columns (1 x 6144 x 8192: 9.3 us, eight waves 10.3), four for many
+    // columns (1 x 50257 x 2048: 15.5 us, two 20.5).  With 64 tokens two tiles do not fit the registers.
+    const int64_t tiles = ((int64_t)a.N + 15) / 16;
+    if (a.T > 32) return linear<GROUP, SB, 1, 64, 8>(a, st);
+    if (a.T > 16) return tiles >= 256 ? linear<GROUP, SB, 2, 32, 8>(a, st) : linear<GROUP, SB, 1, 32, 8>(a, st);
+    if (a.T > 4) return tiles >= 256 ? linear<GROUP, SB, 2, 16, 8>(a, st) : linear<GROUP, SB, 1, 16, 8>(a, st);
+    if (tiles < 256) return linear<GROUP, SB, 1, 4, 8>(a, st);
+    return tiles < 1024 ? linear<GROUP, SB, 2, 4, 16>(a, st) : linear<GROUP, SB, 2, 4, 4>(a, st);
 }
 
 hipError_t launch_linear_q4(const LinearQ4 &a, hipStream_t st)

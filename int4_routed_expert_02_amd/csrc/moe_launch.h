@@ -4,7 +4,21 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
+
+// More dynamic LDS than the 64 KB a kernel gets unasked: asked for once per device
+// (`done`: one bit each, beside the kernel).
+inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return hipErrorInvalidDevice;
+    if (done.load(std::memory_order_relaxed) >> dev & 1) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
 
 struct FfnArgs {
     const void *A;  // rows: bf16 activations (gate/up) or f16 h (down)

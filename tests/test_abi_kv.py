@@ -128,6 +128,8 @@ def test_kv_arguments(moe):
     (dict(K=1000, stride=1000), -2),
     (dict(group=16), -3),
     (dict(group=256), -3),
+    (dict(K=(1 << 26) + 32, stride=1 << 27), -3),
+    (dict(stride=(1 << 25) + 8), -3),
     (dict(stride=1016), -2),
     (dict(fmt=2), -2),
     (dict(T=0), 0),

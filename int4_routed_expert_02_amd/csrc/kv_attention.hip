@@ -56,9 +56,18 @@ __device__ __forceinline__ void split_bf16x2(float e0, float e1, uint32_t &hi, u
                     e1 - __uint_as_float(__float_as_uint(e1) & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ float uniform(float v)
+// Eight int8 codes to bf16: small integers are their f32's upper halves.
+__device__ __forceinline__ u32x4 codes_bf16(u32x2 w)
 {
-    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+    u32x4 r;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const int32_t v = (int32_t)w[d];
+        const float f0 = (float)((v << 24) >> 24), f1 = (float)((v << 16) >> 24), f2 = (float)((v << 8) >> 24), f3 = (float)(v >> 24);
+        r[2 * d] = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+        r[2 * d + 1] = __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+    }
+    return r;
 }
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
@@ -289,7 +298,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         const u32x4 w = kq[u][k >> 1];
-                        const u32x4 kb = unpack_int8x8((k & 1) ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]});
+                        const u32x4 kb = codes_bf16((k & 1) ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]});
 #pragma unroll
                         for (int n = 0; n < NT; ++n) z[n][u] = mfma_bf16(kb, q[n][k], z[n][u]);
                     }
@@ -302,7 +311,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
                 softmax(z, valid ? ks * zscale : 0.f, valid ? vs : 0.f, b0, full, valid, p);
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    const u32x4 vb[2] = {unpack_int8x8(u32x2{vq[d][0], vq[d][1]}), unpack_int8x8(u32x2{vq[d][2], vq[d][3]})};
+                    const u32x4 vb[2] = {codes_bf16(u32x2{vq[d][0], vq[d][1]}), codes_bf16(u32x2{vq[d][2], vq[d][3]})};
                     values(d, vb, p);
                 }
                 if (!more) break;
@@ -455,9 +464,11 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
 
 // ---------------------------------------------------------------- many rows
 
-constexpr int TILE_WAVES = 4, TILE_ROWS = 32 * TILE_WAVES;  // query rows of a workgroup, 32 a wave
+// Waves of a workgroup, 32 query rows each.
+constexpr int tile_waves(int dim) { return dim == 64 ? 4 : 8; }
 
-constexpr int TILE_MIN = 8;                                 // tiles of 64 positions in a part, at least
+constexpr int TILE_TARGET = 512;  // workgroups of the many-row kernel that fill the chip
+constexpr int TILE_MIN = 8;  // tiles of 64 positions in a part, at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -467,17 +478,17 @@ __device__ __forceinline__ f32x16 mfma32_bf16(u32x4 a, u32x4 b, f32x16 c)
                                                    0);
 }
 
-// The tiles that the query rows [128 rt, 128 rt + 128) of a sequence and head
-// look at, and how they are cut into parts.
+// The tiles that the rt-th `rows` query rows of a sequence and head look at, and
+// how they are cut into parts.
 struct RowTile {
     int lo, hi;         // positions some row sees lie in [lo, hi)
     int t0, total;      // first tile's position, tiles
     int parts, per;
 };
 
-__device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, int group, int rt, int ns)
+__device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, int group, int rt, int rows, int ns)
 {
-    const int i0 = rt * TILE_ROWS / group, i1 = min((rt * TILE_ROWS + TILE_ROWS - 1) / group, sq.n - 1);
+    const int i0 = rt * rows / group, i1 = min((rt * rows + rows - 1) / group, sq.n - 1);
     RowTile t;
     int x;
     kv_sees(a, sq, L, i0, t.lo, x);
@@ -495,28 +506,31 @@ __device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, in
 //      which is what the second product takes from a lane; 16-byte units of a row XORed with
 //      the row, so that the 32 rows of an operand read lie on different banks;
 //   V  [D rows][64 positions] bf16, 16-byte units XORed with the row;
-//   per chunk of 16 positions: score scale, value scale (negative where the chunk is absent), its
-//   log2 and inverse.
+//   of each of the tile's four chunks of 16 positions: score scales, log2 of the value scales, their
+//   inverses, the value scales (negative where the chunk is absent); whether no scale needs care.
 template <int D>
 struct TileLds {
-    static constexpr int KB = 64 * D * 2, BYTES = 2 * KB + 64;
+    static constexpr int KB = 64 * D * 2, BYTES = 2 * KB + 80;
     char *base;
     __device__ u32x4 *k(int buf, int row, int unit) const
     {
-        return (u32x4 *)(base + buf * BYTES + row * D * 2 + ((unit ^ (row & 7)) << 4));
+        return (u32x4 *)(base + buf * BYTES + row * D * 2 + ((unit ^ (row & (D / 8 - 1))) << 4));
     }
     __device__ u32x4 *v(int buf, int d, int unit) const
     {
         return (u32x4 *)(base + buf * BYTES + KB + d * 128 + ((unit ^ (d & 7)) << 4));
     }
-    __device__ float *chunk(int buf, int c) const { return (float *)(base + buf * BYTES + 2 * KB) + c * 4; }
+    __device__ f32x4 *chunks(int buf) const { return (f32x4 *)(base + buf * BYTES + 2 * KB); }
 };
 
 template <int D, int BITS>
-__global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles)
+__global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles)
 {
     constexpr int QS = D / 16, DT = D / 32;     // contraction steps of a score, d tiles
-    constexpr int NR = D / 64 * (BITS / 8);     // 16-byte pieces of K (and of V) a thread stages
+    constexpr int TW = tile_waves(D), TILE_ROWS = 32 * TW, THREADS = TW * WAVE;
+    // What a thread stages of a tile: KC values of one position's K, and 8 * VU positions of VN rows of V.
+    constexpr int KC = D / TW, VN = KC > 16 ? KC / 16 : 1, VU = KC / 8 / VN, VP = 8 / VU;  // VP threads a row of V
+    static_assert(KC % 8 == 0 && VU <= 2, "");
     extern __shared__ __align__(16) char tile_lds[];
     const TileLds<D> lds{tile_lds};
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h32 = lane >> 5, c32 = lane & 31;
@@ -526,12 +540,16 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
     b /= a.kv_heads;
     const int split = b % t.ns;
     b /= t.ns;
-    const int s = b % a.n_seq, rt = row_tiles - 1 - b / a.n_seq;
+    const int s = b % a.n_seq;
+    int rt = row_tiles - 1 - b / a.n_seq;
+    // a grid that is all there at once, two workgroups a compute unit: the second half goes up from the
+    // shortest rows, so that the longest share a unit with the shortest
+    if (gridDim.x <= TILE_TARGET && rt < row_tiles / 2) rt = row_tiles / 2 - 1 - rt;
     const KvSeq sq = kv_seq(a, s);
     const int rows = sq.n * t.group;
     if (rt * TILE_ROWS >= rows) return;
     const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
-    const RowTile tl = row_tile(a, sq, L, t.group, rt, t.ns);
+    const RowTile tl = row_tile(a, sq, L, t.group, rt, TILE_ROWS, t.ns);
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
     const int F = BITS == 8 ? (L >> log2p) << log2p : 0;  // from here on: the open page
@@ -564,12 +582,13 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
         for (int j = 0; j < 16; ++j) o[d][j] = 0.f;
     float m = M_NONE, l = 0.f;
 
-    // ---- staging: thread tid has position tid / 4 of a tile's K (a quarter of its values) and, of V,
-    // rows d = tid / 4 (+ 64) and chunk tid % 4
-    const int kt = tid >> 2, kq = tid & 3, vd = tid >> 2, vc = tid & 3;
-    u32x4 kr[NR], vr[NR];
-    float ks = 0.f, vs = 0.f;  // this lane's chunk (tid % 4)
-    int idk = -1, idv = -1;    // pages of the K position and of the V chunk of the tile to load next
+    // ---- staging
+    const int kt = tid / TW, kq = tid % TW;                             // position, part of its values
+    const int vd = tid / VP, vt = (tid % VP) * (8 * VU), vc = vt >> 4;  // row (+ THREADS / VP each), first position, its chunk
+    typedef uint32_t raw_t __attribute__((ext_vector_type(2 * (BITS / 8))));  // eight values
+    raw_t kr[KC / 8], vr[VN * VU];
+    float ks = 0.f, vs = 0.f;            // wave 0: chunk lane % 4
+    int idk = -1, idv = -1, idc = -1;    // pages of the position, of the V chunk, of chunk lane % 4 of the tile to load next
     auto page_of = [&](int tile, int chunk) {
         const int j = tl.t0 + 64 * tile + 16 * chunk;
         return j < L ? kv_page(a, s, j >> log2p) : -1;
@@ -577,27 +596,44 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
     auto ids_of = [&](int tile) {
         idk = page_of(tile, kt >> 4);
         idv = page_of(tile, vc);
+        if (wave == 0) idc = page_of(tile, lane & 3);
     };
     const int64_t page_elems = ((int64_t)a.kv_heads * D) << log2p, head_at = (int64_t)kh * D << log2p;
     constexpr int EB = BITS / 8;
     auto load = [&](int tile) {
-        const int jk = tl.t0 + 64 * tile + kt, jv = tl.t0 + 64 * tile + 16 * vc;
-        const char *sk = (const char *)a.k + (max(idk, 0) * page_elems + head_at + (jk & (P - 1)) * D + kq * (D / 4)) * EB;
+        const int jk = tl.t0 + 64 * tile + kt, jv = tl.t0 + 64 * tile + vt;
+        const char *sk = (const char *)a.k + (max(idk, 0) * page_elems + head_at + (jk & (P - 1)) * D + kq * KC) * EB;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) kr[n] = *(const u32x4 *)(sk + 16 * n);
+        for (int n = 0; n < KC / 8; ++n) kr[n] = *(const raw_t *)(sk + 8 * n * EB);
         const char *sv = (const char *)a.v + (max(idv, 0) * page_elems + head_at + (vd << log2p) + (jv & (P - 1))) * EB;
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n)
+        for (int n = 0; n < VN; ++n)
 #pragma unroll
-            for (int u = 0; u < EB; ++u) vr[n * EB + u] = *(const u32x4 *)(sv + ((int64_t)(64 * n) << log2p) * EB + 16 * u);
-        if (BITS == 8) {
-            ks = idv >= 0 ? a.k_scale[(int64_t)idv * a.kv_heads + kh] : 0.f;
-            vs = idv >= 0 ? a.v_scale[(int64_t)idv * a.kv_heads + kh] : 0.f;
+            for (int u = 0; u < VU; ++u)
+                vr[n * VU + u] = *(const raw_t *)(sv + (((int64_t)(THREADS / VP * n) << log2p) + 8 * u) * EB);
+        if (BITS == 8 && wave == 0) {
+            ks = a.k_scale[(int64_t)max(idc, 0) * a.kv_heads + kh];
+            vs = a.v_scale[(int64_t)max(idc, 0) * a.kv_heads + kh];
         }
     };
+    auto bf16s = [&](raw_t v) -> u32x4 {
+        if constexpr (BITS == 8) return codes_bf16(v);
+        else return v;
+    };
     const int krow = (kt & 0x33) | ((kt & 4) << 1) | ((kt & 8) >> 1);
+    // wave 0, lanes 0..3: what a chunk's scores and weights are multiplied by
     auto put_chunk = [&](int buf, bool valid, float c, float v) {
-        if (tid < 4) *(f32x4 *)lds.chunk(buf, tid) = f32x4{c, valid ? v : -1.0f, __log2f(v), __builtin_amdgcn_rcpf(v)};
+        if (wave) return;
+        const bool nice = valid && v >= 0x1p-60f && v <= 0x1p60f;
+        const int care = __builtin_amdgcn_ballot_w64(lane < 4 && !nice) ? 1 : 0;
+        if (lane < 4) {
+            float *f = (float *)lds.chunks(buf) + lane;
+            f[0] = c;
+            f[4] = __log2f(v);
+            f[8] = __builtin_amdgcn_rcpf(v);
+            f[12] = valid ? v : -1.0f;
+            if (lane == 0) f[16] = __int_as_float(care);
+        }
     };
     // Eight bf16 values from position j on, 0 in the place of those no row here
     // sees: these may hold anything, and 0 * NaN is not 0.
@@ -610,89 +646,73 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
         return v;
     };
     auto put = [&](int buf, int tile) {
-        if (BITS == 16) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n) *lds.k(buf, krow, kq * NR + n) = kr[n];
-            const int j = tl.t0 + 64 * tile + 16 * vc;
-            const bool whole = idv >= 0 && j >= tl.lo && j + 16 <= tl.hi;
+        for (int n = 0; n < KC / 8; ++n) *lds.k(buf, krow, kq * (KC / 8) + n) = bf16s(kr[n]);
+        const int j = tl.t0 + 64 * tile + vt;
+        const bool whole = BITS == 8 || (idv >= 0 && j >= tl.lo && j + 8 * VU <= tl.hi);
 #pragma unroll
-            for (int n = 0; n < D / 64; ++n)
+        for (int n = 0; n < VN; ++n)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    *lds.v(buf, vd + 64 * n, 2 * vc + u) = whole ? vr[n * 2 + u]
-                                                           : idv < 0 ? u32x4{0, 0, 0, 0} : seen(vr[n * 2 + u], j + 8 * u);
-            put_chunk(buf, idv >= 0, zscale, 1.0f);
-            return;
-        }
-#pragma unroll
-        for (int n = 0; n < D / 64; ++n)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                *lds.k(buf, krow, 2 * (kq * (D / 64) + n) + u) = unpack_int8x8(u32x2{kr[n][2 * u], kr[n][2 * u + 1]});
-                *lds.v(buf, vd + 64 * n, 2 * vc + u) = unpack_int8x8(u32x2{vr[n][2 * u], vr[n][2 * u + 1]});
+            for (int u = 0; u < VU; ++u) {
+                u32x4 v = bf16s(vr[n * VU + u]);
+                if (BITS == 16 && !whole) v = idv < 0 ? u32x4{0, 0, 0, 0} : seen(v, j + 8 * u);
+                *lds.v(buf, vd + THREADS / VP * n, (vt >> 3) + u) = v;
             }
-        put_chunk(buf, idv >= 0, ks * zscale, vs);
+        if (BITS == 8) put_chunk(buf, idc >= 0, ks * zscale, vs);
+        else put_chunk(buf, idc >= 0, zscale, 1.0f);
     };
     // a tile with chunks of the open page, loaded where it is needed
     auto put_open = [&](int buf, int tile) {
-        const int b0 = tl.t0 + 64 * tile, jk = b0 + kt, jv = b0 + 16 * vc;
+        const int b0 = tl.t0 + 64 * tile, jk = b0 + kt, jv = b0 + vt;
         const bool openk = jk >= F, openv = jv >= F;
-        if (idk >= 0 && openk && slot >= 0) {
-            const uint16_t *src = a.k_tail + kv_block_at(a, (int64_t)slot * 2 + ((jk >> log2p) & 1), kh) + (jk & (P - 1)) * D;
 #pragma unroll
-            for (int n = 0; n < D / 32; ++n) *lds.k(buf, krow, kq * (D / 32) + n) = *(const u32x4 *)(src + kq * (D / 4) + 8 * n);
-        } else {
-            const char *src = (const char *)a.k + idk * page_elems + head_at + (jk & (P - 1)) * D + kq * (D / 4);
-#pragma unroll
-            for (int n = 0; n < D / 32; ++n)
-                *lds.k(buf, krow, kq * (D / 32) + n) =
-                    idk >= 0 && !openk ? unpack_int8x8(*(const u32x2 *)(src + 8 * n)) : u32x4{0, 0, 0, 0};
-        }
-        const bool valid = idv >= 0 && (!openv || slot >= 0);
-        float cks = 1.f, cvs = 1.f;
-        if (valid && !openv) {
-            cks = a.k_scale[(int64_t)idv * a.kv_heads + kh];
-            cvs = a.v_scale[(int64_t)idv * a.kv_heads + kh];
+        for (int n = 0; n < KC / 8; ++n) {
+            const int at = (jk & (P - 1)) * D + kq * KC + 8 * n;
+            u32x4 v = {0, 0, 0, 0};
+            if (idk >= 0 && openk && slot >= 0)
+                v = *(const u32x4 *)(a.k_tail + kv_block_at(a, (int64_t)slot * 2 + ((jk >> log2p) & 1), kh) + at);
+            else if (idk >= 0 && !openk)
+                v = codes_bf16(*(const u32x2 *)((const char *)a.k + idk * page_elems + head_at + at));
+            *lds.k(buf, krow, kq * (KC / 8) + n) = v;
         }
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n)
+        for (int n = 0; n < VN; ++n)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int at = ((vd + 64 * n) << log2p) + (jv & (P - 1)) + 8 * u;
+            for (int u = 0; u < VU; ++u) {
+                const int at = ((vd + THREADS / VP * n) << log2p) + (jv & (P - 1)) + 8 * u;
                 u32x4 v = {0, 0, 0, 0};
-                if (valid && openv)
+                if (idv >= 0 && openv && slot >= 0)
                     v = seen(*(const u32x4 *)(a.v_tail + kv_block_at(a, (int64_t)slot * 2 + ((jv >> log2p) & 1), kh) + at),
                              jv + 8 * u);
-                else if (valid)
-                    v = unpack_int8x8(*(const u32x2 *)((const char *)a.v + idv * page_elems + head_at + at));
-                *lds.v(buf, vd + 64 * n, 2 * vc + u) = v;
+                else if (idv >= 0 && !openv)
+                    v = codes_bf16(*(const u32x2 *)((const char *)a.v + idv * page_elems + head_at + at));
+                *lds.v(buf, vd + THREADS / VP * n, (vt >> 3) + u) = v;
             }
+        const bool openc = b0 + 16 * (lane & 3) >= F, valid = idc >= 0 && (!openc || slot >= 0);
+        float cks = 1.f, cvs = 1.f;
+        if (valid && !openc) {
+            cks = a.k_scale[(int64_t)idc * a.kv_heads + kh];
+            cvs = a.v_scale[(int64_t)idc * a.kv_heads + kh];
+        }
         put_chunk(buf, valid, cks * zscale, cvs);
     };
+
     // ---- one tile: scores, weights, values
     auto step = [&](int buf, int tile) {
         const int b0 = tl.t0 + 64 * tile;
         if (b0 >= hi_max || b0 + 64 <= lo_min) return;  // nothing for this wave
         f32x16 z[2];
 #pragma unroll
-        for (int T = 0; T < 2; ++T) {
+        for (int T = 0; T < 2; ++T)
 #pragma unroll
             for (int j = 0; j < 16; ++j) z[T][j] = 0.f;
 #pragma unroll
-            for (int k = 0; k < QS; ++k) z[T] = mfma32_bf16(*lds.k(buf, 32 * T + c32, 2 * k + h32), q[k], z[T]);
-        }
-        // z[n / 2][8 (n % 2) + j]: chunk n, position b0 + 16 n + 8 h32 + j
-        float c[4], vs[4], lv[4], iv[4];
-        bool all = true;
+        for (int k = 0; k < QS; ++k)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const f32x4 ch = *(const f32x4 *)lds.chunk(buf, n);
-            c[n] = BITS == 8 ? uniform(ch[0]) : zscale;
-            vs[n] = uniform(ch[1]);
-            lv[n] = BITS == 8 ? uniform(ch[2]) : 0.f;
-            iv[n] = BITS == 8 ? uniform(ch[3]) : 1.f;
-            all &= vs[n] >= 0x1p-60f && vs[n] <= 0x1p60f;
-        }
+            for (int T = 0; T < 2; ++T) z[T] = mfma32_bf16(*lds.k(buf, 32 * T + c32, 2 * k + h32), q[k], z[T]);
+        // z[n / 2][8 (n % 2) + j]: chunk n, position b0 + 16 n + 8 h32 + j
+        const f32x4 c = lds.chunks(buf)[0];
+        const int care = __builtin_amdgcn_readfirstlane(*(const int *)(lds.chunks(buf) + 4));
         float xm = -INFINITY;
         auto raise = [&]() {
             if (!__builtin_amdgcn_ballot_w64(xm > m + M_SLACK)) return;
@@ -712,14 +732,15 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
                 p[0][j] = hi_;
                 p[1][j] = lo_;
             }
+            u32x4 vb[DT];
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const u32x4 vb = *lds.v(buf, 32 * d + c32, 2 * n + h32);
+            for (int d = 0; d < DT; ++d) vb[d] = *lds.v(buf, 32 * d + c32, 2 * n + h32);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) o[d] = mfma32_bf16(vb, p[w], o[d]);
-            }
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] = mfma32_bf16(vb[d], p[w], o[d]);
         };
-        if (all && b0 >= lo_all && b0 + 64 <= hi_all) {
+        if (!care && b0 >= lo_all && b0 + 64 <= hi_all) {
             // every row sees every position: the value scale goes into the exponent, and a chunk's
             // sum is divided by it once
 #pragma unroll
@@ -730,23 +751,25 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
                 xm = fmaxf(xm, mx * c[n]);
             }
             raise();
+            const f32x4 lv = lds.chunks(buf)[1], iv = lds.chunks(buf)[2];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float sub = lv[n] - m;
+                const float sub = BITS == 8 ? lv[n] - m : -m;
                 float e[8], sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[n >> 1][(n & 1) * 8 + j], c[n], sub));
                     sum += e[j];
                 }
-                l = __builtin_fmaf(sum, iv[n], l);
+                l = BITS == 8 ? __builtin_fmaf(sum, iv[n], l) : l + sum;
                 values(n, e);
             }
             return;
         }
+        const f32x4 scale = lds.chunks(buf)[3];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const bool valid = !(vs[n] < 0.f);
+            const bool valid = !(scale[n] < 0.f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = b0 + 16 * n + 8 * h32 + j;
@@ -765,7 +788,7 @@ __global__ __launch_bounds__(TILE_WAVES *WAVE, 2) void k_attn_tile(KvArgs a, KvA
                 const float v = z[n >> 1][(n & 1) * 8 + j];
                 e[j] = __builtin_amdgcn_exp2f(v - m);
                 l += e[j];
-                e[j] = v == -INFINITY ? 0.f : e[j] * vs[n];  // 0 * NaN scale
+                e[j] = v == -INFINITY ? 0.f : e[j] * scale[n];  // 0 * NaN scale
             }
             values(n, e);
         }
@@ -838,7 +861,7 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     const int i = (int)(rh / a.q_heads), h = (int)(rh % a.q_heads), d = (int)(idx % (D / 4)) * 4;
     if (i >= sq.n) return;
     const int parts = few ? dec_tiles(a, sq, L, t.ns).parts
-                          : row_tile(a, sq, L, t.group, (i * t.group + h % t.group) / TILE_ROWS, t.ns).parts;
+                          : row_tile(a, sq, L, t.group, (i * t.group + h % t.group) / (32 * tile_waves(D)), 32 * tile_waves(D), t.ns).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;
@@ -876,10 +899,9 @@ static int dec_parts(const KvArgs &a)
 
 static int64_t row_tiles_of(const KvArgs &a)
 {
-    return ((int64_t)a.max_rows * (a.q_heads / a.kv_heads) + TILE_ROWS - 1) / TILE_ROWS;
+    const int rows = 32 * tile_waves(a.head_dim);
+    return ((int64_t)a.max_rows * (a.q_heads / a.kv_heads) + rows - 1) / rows;
 }
-
-constexpr int TILE_TARGET = 512;  // workgroups of the many-row kernel that fill the chip
 
 static int tile_parts(const KvArgs &a)
 {
@@ -919,7 +941,7 @@ static hipError_t attend_many(const KvArgs &a, const KvAttend &t, unsigned grid,
     static std::atomic<uint64_t> done{0};
     const hipError_t e = lds > 64 << 10 ? allow_lds((const void *)k_attn_tile<D, BITS>, (int)lds, done) : hipSuccess;
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3(grid), dim3(TILE_WAVES * WAVE), lds, st, a, t, tiles);
+    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3(grid), dim3(tile_waves(D) * WAVE), lds, st, a, t, tiles);
     return hipGetLastError();
 }
 

@@ -467,8 +467,12 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
 // Waves of a workgroup, 32 query rows each.
 constexpr int tile_waves(int dim) { return dim == 64 ? 4 : 8; }
 
-constexpr int TILE_TARGET = 512;  // workgroups of the many-row kernel that fill the chip
 constexpr int TILE_MIN = 8;  // tiles of 64 positions in a part, at least
+// Workgroups up to which a sequence is cut into parts.  A part's accumulators
+// go through memory: with heads of 128 that costs more than an even load gains
+// (4000 causal rows, 504 workgroups: 195 us whole, 267 in three parts), with
+// heads of 64 less (4096 rows, 512 workgroups: 111 us whole, 87 in three parts).
+constexpr int tile_target(int dim) { return dim == 64 ? 1536 : 512; }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -541,10 +545,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const int split = b % t.ns;
     b /= t.ns;
     const int s = b % a.n_seq;
-    int rt = row_tiles - 1 - b / a.n_seq;
-    // a grid that is all there at once, two workgroups a compute unit: the second half goes up from the
-    // shortest rows, so that the longest share a unit with the shortest
-    if (gridDim.x <= TILE_TARGET && rt < row_tiles / 2) rt = row_tiles / 2 - 1 - rt;
+    const int rt = row_tiles - 1 - b / a.n_seq;
     const KvSeq sq = kv_seq(a, s);
     const int rows = sq.n * t.group;
     if (rt * TILE_ROWS >= rows) return;
@@ -907,7 +908,7 @@ static int tile_parts(const KvArgs &a)
 {
     int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
     const int64_t most = (len / 64 + TILE_MIN) / TILE_MIN, base = (int64_t)a.n_seq * a.kv_heads * row_tiles_of(a);
-    int64_t ns = base > 0 ? TILE_TARGET / base : 1;
+    int64_t ns = base > 0 ? tile_target(a.head_dim) / base : 1;
     if (ns > most) ns = most;
     return (int)(ns < 1 ? 1 : ns);
 }

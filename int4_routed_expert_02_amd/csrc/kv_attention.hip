@@ -151,7 +151,7 @@ struct DecState {
 };
 
 template <int D, int BITS, int NT>
-__global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAttend t)
+__global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k_attn_dec(KvArgs a, KvAttend t)
 {
     constexpr int DT = D / 16, KS = D / 32;  // d tiles, contraction steps of a score
     extern __shared__ __align__(16) float dec_lds[];
@@ -330,66 +330,94 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, 2) void k_attn_dec(KvArgs a, KvAtt
     int first16 = BITS == 8 ? tl.n_codes : 0;
     int tile16 = begin + wave;
     if (tile16 < first16) tile16 += (first16 - tile16 + DEC_WAVES - 1) / DEC_WAVES * DEC_WAVES;
-    for (; tile16 < end; tile16 += DEC_WAVES) {
-        const int b0 = BITS == 8 ? tl.F + 64 * (tile16 - first16) : tl.t0 + 64 * tile16;
+    // The next tile's loads fly while one is used where the registers hold both (heads of 128, 16 rows);
+    // elsewhere the other waves of the SIMD fill the wait.
+    constexpr bool AHEAD = BITS == 16 && D == 128 && NT == 1;
+    if (tile16 < end && (BITS == 16 || a.n_slots > 0)) {
+        const uint16_t *const ka = BITS == 8 ? a.k_tail : (const uint16_t *)a.k;
+        const uint16_t *const va = BITS == 8 ? a.v_tail : (const uint16_t *)a.v;
+        auto first_of = [&](int tile) { return BITS == 8 ? tl.F + 64 * (tile - first16) : tl.t0 + 64 * tile; };
         // the block of a chunk: a page of the cache, or the sequence's open page (only where its id is there)
-        auto block_of = [&](int chunk) -> int64_t {
+        auto block_of = [&](int b0, int chunk) -> int {
             const int j = b0 + 16 * chunk;
             const int id = j < L ? kv_page(a, s, j >> log2p) : -1;
-            if (BITS == 8) return id >= 0 && slot >= 0 ? (int64_t)slot * 2 + ((j >> log2p) & 1) : -1;
+            if (BITS == 8) return id >= 0 && slot >= 0 ? slot * 2 + ((j >> log2p) & 1) : -1;
             return id;
         };
-        const int64_t bk = block_of(kchunk), bg = block_of(g);
-        const bool valid = bg >= 0;
-        const uint16_t *kt = (BITS == 8 ? a.k_tail : (const uint16_t *)a.k) + kv_block_at(a, max(bk, (int64_t)0), kh);
-        const uint16_t *vt = (BITS == 8 ? a.v_tail : (const uint16_t *)a.v) + kv_block_at(a, max(bg, (int64_t)0), kh);
-        const bool have = BITS == 16 || a.n_slots > 0;
         u32x4 kb[4][KS], vb[DT][2];
+        auto load_k = [&](int b0, int block) {
+            const uint16_t *src = ka + kv_block_at(a, max(block, 0), kh) + (((b0 + 16 * kchunk) & (P - 1)) + krow) * D + 16 * g;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-                kb[u][k] = have ? *(const u32x4 *)(kt + (((b0 + 16 * kchunk) & (P - 1)) + krow + 4 * u) * D + 64 * (k >> 1) +
-                                                   16 * g + 8 * (k & 1))
-                                : u32x4{0, 0, 0, 0};
+                for (int k = 0; k < KS; ++k) kb[u][k] = *(const u32x4 *)(src + 4 * u * D + 64 * (k >> 1) + 8 * (k & 1));
+        };
+        auto load_v = [&](int b0, int block) {
+            const uint16_t *src = va + kv_block_at(a, max(block, 0), kh) + (r16 << log2p) + ((b0 + 16 * g) & (P - 1));
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                vb[d][k] = have ? *(const u32x4 *)(vt + ((16 * d + r16) << log2p) + ((b0 + 16 * g) & (P - 1)) + 8 * k)
-                                : u32x4{0, 0, 0, 0};
-        f32x4 z[NT][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                z[n][u] = zero4();
-#pragma unroll
-                for (int k = 0; k < KS; ++k) z[n][u] = mfma_bf16(kb[u][k], q[n][k], z[n][u]);
+                for (int k = 0; k < 2; ++k) vb[d][k] = *(const u32x4 *)(src + ((16 * d) << log2p) + 8 * k);
+        };
+        int b0 = first_of(tile16), bg = block_of(b0, g);
+        if (AHEAD) {
+            load_k(b0, block_of(b0, kchunk));
+            load_v(b0, bg);
+        }
+        while (true) {
+            if (!AHEAD) {
+                bg = block_of(b0, g);
+                load_k(b0, block_of(b0, kchunk));
+                load_v(b0, bg);
             }
-        }
-        const bool full = b0 >= lo_all && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
-        if (!full) {
-            // places that no row sees may hold anything: 0 in their stead, since 0 * NaN is not 0
-            int lo_min, hi_max, y;
-            kv_sees(a, sq, L, 0, lo_min, y);
-            kv_sees(a, sq, L, sq.n - 1, y, hi_max);
+            const int next = tile16 + DEC_WAVES;
+            const bool more = next < end;
+            const int b1 = first_of(next);
+            int bk1 = -1, bg1 = -1;
+            if (AHEAD && more) {
+                bk1 = block_of(b1, kchunk);
+                bg1 = block_of(b1, g);
+            }
+            f32x4 z[NT][4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int j = b0 + 16 * g + 8 * k + 2 * w;
-                    const uint32_t keep = !valid ? 0u
-                                                 : (j >= lo_min && j < hi_max ? 0xFFFFu : 0u) |
-                                                       (j + 1 >= lo_min && j + 1 < hi_max ? 0xFFFF0000u : 0u);
+                for (int n = 0; n < NT; ++n) {
+                    z[n][u] = zero4();
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) vb[d][k][w] &= keep;
+                    for (int k = 0; k < KS; ++k) z[n][u] = mfma_bf16(kb[u][k], q[n][k], z[n][u]);
                 }
-        }
-        uint32_t p[NT][2][8];
-        softmax(z, zscale, 1.0f, b0, full, valid, p);
+            }
+            if (AHEAD && more) load_k(b1, bk1);
+            const bool valid = bg >= 0;
+            const bool full = b0 >= lo_all && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
+            uint32_t p[NT][2][8];
+            softmax(z, zscale, 1.0f, b0, full, valid, p);
+            if (!full) {
+                // places that no row sees may hold anything: 0 in their stead, since 0 * NaN is not 0
+                int lo_min, hi_max, y;
+                kv_sees(a, sq, L, 0, lo_min, y);
+                kv_sees(a, sq, L, sq.n - 1, y, hi_max);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) values(d, vb[d], p);
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int j = b0 + 16 * g + 8 * k + 2 * w;
+                        const uint32_t keep = !valid ? 0u
+                                                     : (j >= lo_min && j < hi_max ? 0xFFFFu : 0u) |
+                                                           (j + 1 >= lo_min && j + 1 < hi_max ? 0xFFFF0000u : 0u);
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) vb[d][k][w] &= keep;
+                    }
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) values(d, vb[d], p);
+            if (!more) break;
+            if (AHEAD) load_v(b1, bg1);
+            tile16 = next;
+            b0 = b1;
+            bg = bg1;
+        }
     }
 
     // ---- the waves' results together: maxima and sums first, then the accumulators pairwise
@@ -866,14 +894,32 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;
-    float m = M_NONE;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, ml[(p * step + at) * 2]);
-    float l = 0.f;
+    // eight parts' loads at a time are in flight together; a part past the last adds nothing
+    float m = M_NONE, l = 0.f;
     f32x4 o = zero4();
-    for (int p = 0; p < parts; ++p) {
-        const float f = __builtin_amdgcn_exp2f(ml[(p * step + at) * 2] - m);
-        l += ml[(p * step + at) * 2 + 1] * f;
-        o += *(const f32x4 *)(t.part + (p * step + at) * D + d) * f;
+    for (int p0 = 0; p0 < parts; p0 += 8) {
+        float pm[8], pl[8], mn = m;
+        f32x4 po[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t pt = min(p0 + u, parts - 1) * step + at;
+            pm[u] = p0 + u < parts ? ml[pt * 2] : M_NONE;
+            pl[u] = p0 + u < parts ? ml[pt * 2 + 1] : 0.f;
+            po[u] = *(const f32x4 *)(t.part + pt * D + d);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, pm[u]);
+        const float f0 = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f0;
+        o *= f0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (p0 + u >= parts) break;
+            const float f = __builtin_amdgcn_exp2f(pm[u] - m);
+            l += pl[u] * f;
+            o += po[u] * f;
+        }
     }
     o *= l == 0.f ? 0.f : 1.0f / l;
     if (t.out_f32) *(f32x4 *)((float *)t.out + at * D + d) = o;

@@ -928,6 +928,55 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
 }
 
 
+// The same for few rows and many parts: a workgroup a row and head, its lanes
+// share out the parts.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_parts_few(KvArgs a, KvAttend t)
+{
+    constexpr int LANES = D / 4, PL = 256 / LANES;  // lanes of a row, parts at a time
+    __shared__ f32x4 so[256];
+    __shared__ float sm[PL], sl[PL];
+    const int h = blockIdx.x % a.q_heads, i = (blockIdx.x / a.q_heads) % a.max_rows, s = blockIdx.x / a.q_heads / a.max_rows;
+    const KvSeq sq = kv_seq(a, s);
+    const int L = kv_limit(a, sq), d = threadIdx.x % LANES * 4, pl = threadIdx.x / LANES;
+    if (i >= sq.n) return;
+    const int parts = dec_tiles(a, sq, L, t.ns).parts;
+    if (parts == 1) return;
+    const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
+    const float *ml = t.part + t.ns * step * D;
+    float m = M_NONE, l = 0.f;
+    f32x4 o = zero4();
+    for (int p = pl; p < parts; p += PL) {
+        const int64_t pt = p * step + at;
+        const float pm = ml[pt * 2], pv = ml[pt * 2 + 1];
+        const f32x4 po = *(const f32x4 *)(t.part + pt * D + d);
+        const float mn = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mn), f = __builtin_amdgcn_exp2f(pm - mn);
+        m = mn;
+        l = l * f0 + pv * f;
+        o = o * f0 + po * f;
+    }
+    so[threadIdx.x] = o;
+    if (d == 0) {
+        sm[pl] = m;
+        sl[pl] = l;
+    }
+    __syncthreads();
+    if (pl) return;
+    for (int u = 1; u < PL; ++u) m = fmaxf(m, sm[u]);
+    l = 0.f;
+    o = zero4();
+#pragma unroll
+    for (int u = 0; u < PL; ++u) {
+        const float f = __builtin_amdgcn_exp2f(sm[u] - m);
+        l += sl[u] * f;
+        o += so[u * LANES + threadIdx.x] * f;
+    }
+    o *= l == 0.f ? 0.f : 1.0f / l;
+    if (t.out_f32) *(f32x4 *)((float *)t.out + at * D + d) = o;
+    else *(u32x2 *)((uint16_t *)t.out + at * D + d) = u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
+    if (t.lse && d == 0) t.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * (1.0f / LOG2E);
+}
+
 // ---------------------------------------------------------------- launches
 
 constexpr int DEC_TARGET = 512;  // workgroups that fill the chip: 2 per compute unit
@@ -1005,6 +1054,12 @@ static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
         e = attend_many<D, BITS>(a, t, (unsigned)grid, (int)tiles, st);
     }
     if (e != hipSuccess || t.ns == 1) return e;
+    // more than one round of loads for a lane that takes all parts
+    const int64_t each = (int64_t)a.n_seq * a.max_rows * a.q_heads;
+    if (few_rows(a) && t.ns > 8 && each <= 65536) {
+        hipLaunchKernelGGL((k_attn_parts_few<D>), dim3((unsigned)each), dim3(256), 0, st, a, t);
+        return hipGetLastError();
+    }
     const int64_t groups = ((int64_t)a.max_rows * a.q_heads * (D / 4) + 255) / 256;
     hipLaunchKernelGGL((k_attn_parts<D>), dim3((unsigned)(groups * a.n_seq)), dim3(256), 0, st, a, t, (int)groups,
                        few_rows(a) ? 1 : 0);

@@ -466,13 +466,13 @@ typedef struct {
     int32_t n_seq;       /* sequences of the batch, >= 0 */
     int32_t rows;        /* rows (new tokens) of all sequences, >= 0 */
     int32_t max_rows;    /* no sequence has more rows than this (rows beyond it are left out), 0..rows */
-    int32_t max_len;     /* no kv_len is above this (positions from it on are left out), >= 0 */
+    int32_t max_len;     /* no kv_len is above this (positions from it on are left out), 0..2^30 */
     int32_t q_heads, kv_heads; /* q head h reads key/value head h / (q_heads / kv_heads) */
     int32_t head_dim;    /* 64 or 128 */
     int32_t kv_bits;     /* 8 or 16 */
     int32_t page_tokens; /* 16, 32, 64 or 128 */
     int32_t n_pages;     /* pages of the cache */
-    int32_t max_pages;   /* row length of the page table */
+    int32_t max_pages;   /* row length of the page table; max_pages * page_tokens at most 2^30 */
     int32_t n_slots;     /* kv_bits 8: sequences that have open pages */
     int32_t window;      /* > 0: a row at position p sees positions above p - window only; 0: all */
     float scale;         /* scores are scale * q.k; 0: 1 / sqrt(head_dim) */
@@ -508,7 +508,8 @@ typedef struct {
  *         rotated by its position ((a, b) -> (a cos - b sin, a sin + b cos), computed
  *         in f32), rounded to bf16 and stored; v is stored as it is
  *   q     nullable, [rows][q_heads][head_dim] bf16, row stride q_row_stride: normed and
- *         rotated like k into q_out [rows][q_heads][head_dim], which may be q itself
+ *         rotated like k into q_out [rows][q_heads][head_dim], which may be q itself (its
+ *         rows q_heads * head_dim apart)
  *   rot   nullable: no norm and no rotation
  * Different sequences of a call must not share a page that the call writes, or a slot.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (head_dim, page_tokens or
@@ -535,6 +536,7 @@ int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batch, const mo
  *   q    [rows][q_heads][head_dim] bf16, row stride q_row_stride (moe_kv_append's q_out)
  *   out  [rows][q_heads][head_dim] bf16, or f32 with MOE_OUT_F32
  *   lse  nullable, [rows][q_heads] f32 (natural log)
+ * out and lse must not overlap q.  Rows that belong to no sequence are left as they are.
  *   ws   moe_kv_workspace_bytes(shape) bytes, 256-byte aligned (parts of a long sequence)
  * Errors as moe_kv_append, and MOE_ERR_WORKSPACE.
  */

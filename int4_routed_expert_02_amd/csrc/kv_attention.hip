@@ -492,15 +492,26 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
 
 // ---------------------------------------------------------------- many rows
 
+constexpr int TILE_MIN = 8;  // tiles of 64 positions in a part, at least
+
+// The sequence that is r-th by length, longest first (ties in their order): its
+// workgroups are started first, so that no long one is left for the end.  Up to 64
+// sequences; more go in their order.
+__device__ __forceinline__ int kv_ranked(const KvArgs &a, int r, int lane)
+{
+    if (a.n_seq > WAVE || a.n_seq == 1) return r;
+    const int len = lane < a.n_seq ? a.kv_len[lane] : INT32_MIN;
+    int rank = 0;
+    for (int j = 0; j < a.n_seq; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane) ? 1 : 0;
+    }
+    return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.n_seq && rank == r));
+}
+
 // Waves of a workgroup, 32 query rows each.
 constexpr int tile_waves(int dim) { return dim == 64 ? 4 : 8; }
 
-constexpr int TILE_MIN = 8;  // tiles of 64 positions in a part, at least
-// Workgroups up to which a sequence is cut into parts.  A part's accumulators
-// go through memory: with heads of 128 that costs more than an even load gains
-// (4000 causal rows, 504 workgroups: 195 us whole, 267 in three parts), with
-// heads of 64 less (4096 rows, 512 workgroups: 111 us whole, 87 in three parts).
-constexpr int tile_target(int dim) { return dim == 64 ? 1536 : 512; }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -518,8 +529,9 @@ struct RowTile {
     int parts, per;
 };
 
-__device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, int group, int rt, int rows, int ns)
+__device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, const KvAttend &at, int rt, int rows)
 {
+    const int group = at.group;
     const int i0 = rt * rows / group, i1 = min((rt * rows + rows - 1) / group, sq.n - 1);
     RowTile t;
     int x;
@@ -527,7 +539,7 @@ __device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, in
     kv_sees(a, sq, L, i1, x, t.hi);
     t.t0 = t.lo & ~63;
     t.total = t.hi > t.t0 ? (t.hi - t.t0 + 63) >> 6 : 0;
-    t.parts = max(1, min(ns, (t.total + TILE_MIN - 1) / TILE_MIN));
+    t.parts = max(1, min(at.ns, (t.total + TILE_MIN - 1) / TILE_MIN));
     t.per = (t.total + t.parts - 1) / t.parts;
     return t;
 }
@@ -566,19 +578,23 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     extern __shared__ __align__(16) char tile_lds[];
     const TileLds<D> lds{tile_lds};
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h32 = lane >> 5, c32 = lane & 31;
-    // kv head fastest (a head's workgroups share an L2), the last rows (the longest, if causal) first
+    // kv head fastest (a head's workgroups share an L2), then the longest rows first: where most positions
+    // are cached ones, a long sequence's rows before a shorter one's (2 x 2048 rows over 16384 and 8465
+    // positions: 1009 us, 1250 with the sequences in turn), else the last rows of every sequence (3 x 1000
+    // rows: 32 us, 36 by sequences)
     int b = blockIdx.x;
     const int kh = b % a.kv_heads;
     b /= a.kv_heads;
     const int split = b % t.ns;
     b /= t.ns;
-    const int s = b % a.n_seq;
-    const int rt = row_tiles - 1 - b / a.n_seq;
+    const bool by_length = a.max_len / 2 >= a.max_rows;
+    const int s = kv_ranked(a, by_length ? b / row_tiles : b % a.n_seq, lane);
+    const int rt = row_tiles - 1 - (by_length ? b % row_tiles : b / a.n_seq);
     const KvSeq sq = kv_seq(a, s);
     const int rows = sq.n * t.group;
     if (rt * TILE_ROWS >= rows) return;
     const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
-    const RowTile tl = row_tile(a, sq, L, t.group, rt, TILE_ROWS, t.ns);
+    const RowTile tl = row_tile(a, sq, L, t, rt, TILE_ROWS);
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
     const int F = BITS == 8 ? (L >> log2p) << log2p : 0;  // from here on: the open page
@@ -890,7 +906,7 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     const int i = (int)(rh / a.q_heads), h = (int)(rh % a.q_heads), d = (int)(idx % (D / 4)) * 4;
     if (i >= sq.n) return;
     const int parts = few ? dec_tiles(a, sq, L, t.ns).parts
-                          : row_tile(a, sq, L, t.group, (i * t.group + h % t.group) / (32 * tile_waves(D)), 32 * tile_waves(D), t.ns).parts;
+                          : row_tile(a, sq, L, t, (i * t.group + h % t.group) / (32 * tile_waves(D)), 32 * tile_waves(D)).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;
@@ -999,11 +1015,17 @@ static int64_t row_tiles_of(const KvArgs &a)
     return ((int64_t)a.max_rows * (a.q_heads / a.kv_heads) + rows - 1) / rows;
 }
 
+// Parts that the positions of a many-row call are cut into, as long as its
+// workgroups are fewer than this.  A part's accumulators go through memory: with heads of 128
+// that costs more than an even load gains once the chip is full (4000 causal rows, 504
+// workgroups: 195 us whole, 267 in three parts), with heads of 64 less (4096 causal rows, 512
+// workgroups: 111 us whole, 87 in three parts).
 static int tile_parts(const KvArgs &a)
 {
-    int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
+    const int64_t target = a.head_dim == 64 ? 1536 : 512;
+    const int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
     const int64_t most = (len / 64 + TILE_MIN) / TILE_MIN, base = (int64_t)a.n_seq * a.kv_heads * row_tiles_of(a);
-    int64_t ns = base > 0 ? tile_target(a.head_dim) / base : 1;
+    int64_t ns = base > 0 ? target / base : 1;
     if (ns > most) ns = most;
     return (int)(ns < 1 ? 1 : ns);
 }

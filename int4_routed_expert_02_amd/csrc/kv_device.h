@@ -14,7 +14,7 @@ struct KvSeq {
     int row0;   // first row in the batch's tensors
     int n;      // rows, inside the batch's tensors and at most max_rows
     int n_pos;  // rows as the table has them: row i has position len - n_pos + i
-    int len;    // kv_len as the table has it, at least 0
+    int len;    // kv_len as the table has it, from 0 to 2^30
 };
 
 __device__ __forceinline__ KvSeq kv_seq(const KvArgs &a, int s)
@@ -25,7 +25,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs &a, int s)
     const int n = max(min(r1, a.rows) - q.row0, 0);
     q.n = min(n, a.max_rows);
     q.n_pos = n;
-    q.len = max(a.kv_len[s], 0);
+    q.len = min(max(a.kv_len[s], 0), 1 << 30);
     return q;
 }
 

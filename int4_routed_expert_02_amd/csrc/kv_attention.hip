@@ -5,13 +5,13 @@
 // pass over the cache with a running m, sum and accumulator (each rescaled
 // when m grows), all in f32.
 //
-// Both kernels compute S^T = K Q^T and O^T = V^T P^T on the matrix cores, so a
-// lane holds scores of one query row: the weights of a row go from the first
-// product's accumulator into the second product's operand without leaving the
-// lane.  The rows of the K operand are taken in an order that makes each lane's
-// scores belong to consecutive positions, so a lane reads V^T (stored [D][P])
-// in 16-byte pieces of 16 consecutive positions, which lie in one page whatever
-// its size, with one pair of scales.
+// Both kernels, the one for few rows and the one for many, compute S^T = K Q^T and
+// O^T = V^T P^T on the matrix cores, so a lane holds scores of one query row: the
+// weights of a row go from the first product's accumulator into the second
+// product's operand without leaving the lane.  The rows of the K operand are taken
+// in an order that makes each lane's scores belong to consecutive positions, so a
+// lane reads V^T (stored [D][P]) in 16-byte pieces of 16 consecutive positions,
+// which lie in one page whatever its size, with one pair of scales.
 //
 // An int8 code is exact in bf16, so codes, keys and queries enter the products as
 // they are; a page's key scale (times log2(e) * scale) is applied to its scores in
@@ -19,6 +19,18 @@
 // the sum of two bf16 values, 2^-16 relative at any distance from the maximum.
 // One bf16 value (2^-8) makes an output's error half as large again as its own
 // rounding, and f16 loses weights far below the maximum.
+//
+// What bounds them.  Few rows (k_attn_dec): the cache's bytes.  One row each of 8
+// sequences of 75639..131072 positions, 8 x 128 in 8 bits: 1.69 GB in 303 us, 5.6 TB/s; three to
+// five drafted rows of 16 sequences, a window of 8192 positions of 8 x 128 in bf16: 0.54 GB in
+// 109 us, 5.0 TB/s; 32 sequences of 2324..4096 positions, 4 x 64 in 8 bits: 50 MB in 20 us, a few
+// tiles a wave between two launches.  Many rows (k_attn_tile): vector
+// and matrix instructions together.  Two waves on one SIMD overlap them only in part
+// (118 us of products and 144 us of vector work alone take 233 us side by side), so a
+// tile costs about its vector work and 0.7 of its products: 720 TFLOP/s (the weights'
+// second halves not counted) for 3707 rows over 16384 and 8465 positions with heads of
+// 128, 400 for a causal prompt of 4096 rows with heads of 64, whose softmax is twice as
+// large a share.
 #include "kv_device.h"
 
 namespace moe {
@@ -88,6 +100,7 @@ struct DecTiles {
     int t0, F, n_codes, total, parts, per;
 };
 
+// Waves of a workgroup: they take a part's tiles in turn, and join their results in LDS.
 constexpr int DEC_WAVES = 8;
 
 __device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, int L, int ns)
@@ -510,8 +523,9 @@ __device__ __forceinline__ int kv_ranked(const KvArgs &a, int r, int lane)
 }
 
 // Waves of a workgroup, 32 query rows each.
+// With heads of 128 eight share a tile's staging (2048 and 1659 rows over 16384 and 8465 positions: 1049 us,
+// four 1127); with heads of 64 four leave two workgroups a compute unit (a prompt of 4096 rows: 88 us, eight 120).
 constexpr int tile_waves(int dim) { return dim == 64 ? 4 : 8; }
-
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -579,8 +593,8 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const TileLds<D> lds{tile_lds};
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h32 = lane >> 5, c32 = lane & 31;
     // kv head fastest (a head's workgroups share an L2), then the longest rows first: where most positions
-    // are cached ones, a long sequence's rows before a shorter one's (2 x 2048 rows over 16384 and 8465
-    // positions: 1009 us, 1250 with the sequences in turn), else the last rows of every sequence (3 x 1000
+    // are cached ones, a long sequence's rows before a shorter one's (2048 and 1659 rows over 16384 and
+    // 8465 positions: 1009 us, 1250 with the sequences in turn), else the last rows of every sequence (3 x 1000
     // rows: 32 us, 36 by sequences)
     int b = blockIdx.x;
     const int kh = b % a.kv_heads;
@@ -1076,7 +1090,8 @@ static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
         e = attend_many<D, BITS>(a, t, (unsigned)grid, (int)tiles, st);
     }
     if (e != hipSuccess || t.ns == 1) return e;
-    // more than one round of loads for a lane that takes all parts
+    // More than one round of loads for a lane that takes all parts, so the parts go over lanes (one
+    // sequence of 30000 positions: 12.8 us, 19.9 in one lane).
     const int64_t each = (int64_t)a.n_seq * a.max_rows * a.q_heads;
     if (few_rows(a) && t.ns > 8 && each <= 65536) {
         hipLaunchKernelGGL((k_attn_parts_few<D>), dim3((unsigned)each), dim3(256), 0, st, a, t);

@@ -17,12 +17,10 @@
 // against a constant whose result is where the group's accumulators start.  The
 // scale (times 16) joins a group's sum in f32.
 //
-// What it reaches: 5 x 50257 x 2048, 58 MB in 15.3 us, 3.8 TB/s (reading alone in this
-// pattern takes 10.4 us): six workgroups a compute unit in turn, each with the
-// latency of its first loads and its last sums.  32 x 6144 x 8192, 26 MB in 15.6 us: every
-// workgroup reads all activations (100 MB from the L2s); without products and
-// activations the weights take 9.5 us.  1 x 1536 x 1024 takes 3 us on the device and is
-// bound by the call.
+// What it reaches: 5 x 50257 x 2048, 58 MB in 14.7 us, 4.0 TB/s (reading alone in this
+// pattern takes 10.4 us).  32 x 6144 x 8192, 26 MB in 14.4 us: every workgroup reads all
+// activations (100 MB from the L2s); without products and activations the weights take
+// 9.5 us.  1 x 1536 x 1024 takes 3 us on the device and is bound by the call.
 #include <type_traits>
 
 #include "moe_device.h"
@@ -58,70 +56,103 @@ __device__ __forceinline__ u32x4 lq_transpose(u32x4 v)
 // wave's activations (TR rows of a block of 128 k) and scales come in runs
 // along k and go through a piece of LDS of its own: no barriers, so the
 // waves drift apart and one loads while another computes.
-template <int GROUP, int RT, int TR, int WAVES>
+//
+// More than 16 tokens, where 16 bytes of a column's scales last for four blocks: a wave has a run of
+// consecutive blocks and takes their scales in such pieces (32 x 6144 x 8192, bf16 scales of 128: 14.4 us,
+// 15.6 with the waves' blocks in turn and their scales one by one).  Elsewhere the waves take the blocks in
+// turn (5 x 50257 x 2048: 15.3 us against 16.4; 24 x 6144 x 4096, f32 scales of 32: 8.5 against 8.8).
+template <int GROUP, bool SB, int RT, int TR, int WAVES>
 struct LqLds {
     static constexpr int GB = LQ_BLOCK / GROUP, TT = (TR + 15) / 16;
+    static constexpr bool RUNS = TR > 16 && (SB ? 8 : 4) / GB >= 4;
+    static constexpr int NS = RUNS ? (SB ? 8 : 4) : GB, SCB = NS / GB;           // scales of a load, blocks they are for
+    static constexpr int SROW = RUNS ? NS + 1 : GB;                              // a column's scales in LDS
     static constexpr int XROW = LQ_BLOCK * 2 + 16;                               // bytes of a token's row
-    static constexpr int X_BYTES = TR * XROW, WAVE_BYTES = X_BYTES + 16 * RT * GB * 4;
-    static constexpr int R_BYTES = WAVES * RT * TT * 1024;                       // the waves' sums, in the same place at the end
-    static constexpr int BYTES = WAVES * WAVE_BYTES > R_BYTES ? WAVES * WAVE_BYTES : R_BYTES;
+    static constexpr int X_BYTES = TR * XROW, WAVE_BYTES = X_BYTES + 16 * RT * SROW * 4;
+    static constexpr int R_BYTES = WAVES * RT * TT * 1024;                       // the waves' sums
+    // From 5 tokens on, as many workgroups as are resident together take tile after tile of columns, the next
+    // tile's first loads under way while one is summed up (32 x 50257 x 2048: 31 us, 36.5 with a workgroup a
+    // tile; 5 x 50257 x 2048: 14.7, 15.3).  With fewer tokens a workgroup a tile is no slower (1 x 50257 x 2048:
+    // 13.6 us, 14.0 in a loop).
+    static constexpr bool LOOP = RT == 2 && TR >= 16;
+    // in a loop the sums have two places of their own, else they come where the activations were
+    static constexpr int R_AT = LOOP ? WAVES * WAVE_BYTES : 0;
+    static constexpr int BYTES = LOOP ? R_AT + 2 * R_BYTES : WAVES * WAVE_BYTES > R_BYTES ? WAVES * WAVE_BYTES : R_BYTES;
 };
 
-// GB scales from an address of their own alignment
-template <bool SB, int GB>
-__device__ __forceinline__ void lq_scales(const char *p, float (&s)[GB])
+// N scales from an address of their own alignment
+template <bool SB, int N>
+__device__ __forceinline__ void lq_scales(const char *p, float (&s)[N])
 {
     if constexpr (SB) {
-        typedef uint16_t v_t __attribute__((ext_vector_type(GB), aligned(2)));
+        typedef uint16_t v_t __attribute__((ext_vector_type(N), aligned(2)));
         const v_t v = *(const v_t *)p;
 #pragma unroll
-        for (int i = 0; i < GB; ++i) s[i] = bf16_to_f32(v[i]);
+        for (int i = 0; i < N; ++i) s[i] = bf16_to_f32(v[i]);
     } else {
-        typedef float v_t __attribute__((ext_vector_type(GB), aligned(4)));
+        typedef float v_t __attribute__((ext_vector_type(N), aligned(4)));
         const v_t v = *(const v_t *)p;
 #pragma unroll
-        for (int i = 0; i < GB; ++i) s[i] = v[i];
+        for (int i = 0; i < N; ++i) s[i] = v[i];
     }
 }
 
-// 16 * RT columns, up to TR tokens; the workgroup's waves take the blocks of K in turn.
+// 16 * RT columns at a time, up to TR tokens; the workgroup's waves share out the blocks of K.
 template <int GROUP, bool SB, int RT, int TR, int WAVES>
-__global__ __launch_bounds__(WAVES *WAVE) void k_linear_q4(LinearQ4 a, int t0)
+__global__ __launch_bounds__(WAVES *WAVE, TR <= 16 ? 4 : 2) void k_linear_q4(LinearQ4 a, int t0)
 {
-    using Lds = LqLds<GROUP, RT, TR, WAVES>;
+    using Lds = LqLds<GROUP, SB, RT, TR, WAVES>;
     constexpr int TT = Lds::TT, GB = Lds::GB, THREADS = WAVES * WAVE, XU = TR / 4, SS = SB ? 2 : 4;
+    constexpr int NS = Lds::NS, SCB = Lds::SCB, SROW = Lds::SROW;
     extern __shared__ __align__(16) char lq_lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane >> 4, c16 = lane & 15;
     const int tok0 = t0 + blockIdx.y * TR, tokens = min(a.T - tok0, TR);
-    const int n0 = blockIdx.x * 16 * RT, groups = a.K / GROUP, cols = min(16 * RT, a.N - n0);
+    const int groups = a.K / GROUP, tiles = (a.N - 1) / (16 * RT) + 1;
     const int blocks = (a.K + LQ_BLOCK - 1) / LQ_BLOCK;
 
-    // Offsets of the lane's loads from the workgroup's first row: rows past an edge are some row that
-    // is there, and their results are dropped.
-    uint32_t wo[RT], xo[XU];
+    // Offsets of the lane's loads from a tile's first row: rows past an edge are some row that is there,
+    // and their results are dropped.
+    uint32_t wo[RT], xo[XU], so;
+    const char *wbase, *sbase;
+    auto columns = [&](int tile) {
+        const int n0 = tile * 16 * RT, cols = min(16 * RT, a.N - n0);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) wo[r] = (uint32_t)min(16 * r + c16, cols - 1) * (uint32_t)(a.K / 2) + 16 * g;
+        for (int r = 0; r < RT; ++r) wo[r] = (uint32_t)min(16 * r + c16, cols - 1) * (uint32_t)(a.K / 2) + 16 * g;
+        so = (uint32_t)min(lane & (16 * RT - 1), cols - 1) * (uint32_t)(groups * SS);
+        wbase = (const char *)a.q + (int64_t)n0 * (a.K / 2);
+        sbase = (const char *)a.scales + (int64_t)n0 * groups * SS;
+    };
 #pragma unroll
     for (int i = 0; i < XU; ++i) xo[i] = (uint32_t)min(g + 4 * i, tokens - 1) * (uint32_t)(a.x_stride * 2) + 16 * c16;
-    const uint32_t so = (uint32_t)min(lane & (16 * RT - 1), cols - 1) * (uint32_t)(groups * SS);
-    const char *wbase = (const char *)a.q + (int64_t)n0 * (a.K / 2);
     const char *xbase = (const char *)(a.x + (int64_t)tok0 * a.x_stride);
-    const char *sbase = (const char *)a.scales + (int64_t)n0 * groups * SS;
 
     u32x4 w[RT], x[XU];
-    float s[GB];
-    auto load = [&](int b) {
-        const char *wt = wbase + b * (LQ_BLOCK / 2), *xt = xbase + b * (LQ_BLOCK * 2), *st = sbase + b * (GB * SS);
+    float s[NS];
+    // the scales of the SCB blocks from b on, 0 past the last group
+    auto all_scales = [&](int b) { lq_scales<SB, NS>(sbase + so + b * (GB * SS), s); };
+    auto last_scales = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            float v[1];
+            lq_scales<SB, 1>(sbase + so + min(b * GB + i, groups - 1) * SS, v);
+            s[i] = b * GB + i < groups ? v[0] : 0.f;
+        }
+    };
+    auto load = [&](int b, bool scales) {
+        const char *wt = wbase + b * (LQ_BLOCK / 2), *xt = xbase + b * (LQ_BLOCK * 2);
         if ((b + 1) * LQ_BLOCK <= a.K) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) w[r] = *(const u32x4 *)(wt + wo[r]);
 #pragma unroll
             for (int i = 0; i < XU; ++i)
                 if (4 * i < tokens) x[i] = *(const u32x4 *)(xt + xo[i]);
-            lq_scales<SB, GB>(st + so, s);
+            if (scales) {
+                if (SCB == 1 || (b + SCB) * GB <= groups) all_scales(b);
+                else last_scales(b);
+            }
         } else {
-            // the last block ends early: activations and scales are 0 from K on, the codes there are the
+            // the last block ends early: activations (and scales) are 0 from K on, the codes there are the
             // block's first ones (its first 32 are always there)
             const int left = a.K - b * LQ_BLOCK;
 #pragma unroll
@@ -131,12 +162,7 @@ __global__ __launch_bounds__(WAVES *WAVE) void k_linear_q4(LinearQ4 a, int t0)
                 x[i] = *(const u32x4 *)(xt + (8 * c16 < left ? xo[i] : xo[i] - 16 * c16));
                 if (8 * c16 >= left) x[i] = u32x4{0, 0, 0, 0};
             }
-#pragma unroll
-            for (int i = 0; i < GB; ++i) {
-                float v[1];
-                lq_scales<SB, 1>(st + so + (i * GROUP < left ? i * SS : 0), v);
-                s[i] = i * GROUP < left ? v[0] : 0.f;
-            }
+            if (scales) last_scales(b);
         }
     };
     char *const mine = lq_lds + wave * Lds::WAVE_BYTES;
@@ -146,86 +172,108 @@ __global__ __launch_bounds__(WAVES *WAVE) void k_linear_q4(LinearQ4 a, int t0)
 #pragma unroll
         for (int i = 0; i < XU; ++i)
             if (4 * i < tokens) *(u32x4 *)(xput + 4 * i * Lds::XROW) = interleave_bf16x8(x[i]);
+    };
+    auto put_scales = [&]() {
         if (lane < 16 * RT) {
 #pragma unroll
-            for (int i = 0; i < GB; ++i) sc[lane * GB + i] = s[i] * 16.0f;
+            for (int i = 0; i < NS; ++i) sc[lane * SROW + i] = s[i] * 16.0f;
         }
     };
 
-    f32x4 y[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) y[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const u32x4 offset = {0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u};  // -1.5
     const char *xget[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) xget[t] = mine + min(16 * t + c16, tokens - 1) * Lds::XROW + 16 * g;
 
-    if (wave < blocks) load(wave);
-    for (int b = wave; b < blocks; b += WAVES) {
-        put();
-        // the wave's own writes, read by its other lanes: LDS keeps their order, the compiler is told to
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        u32x4 wb[RT];
+    const int per = (blocks + WAVES - 1) / WAVES;
+    const int b0 = Lds::RUNS ? wave * per : wave, b1 = Lds::RUNS ? min(blocks, b0 + per) : blocks;
+    constexpr int STEP = Lds::RUNS ? 1 : WAVES;
+    const int stride = gridDim.x;
+    int tile = blockIdx.x;
+    columns(tile);
+    if (b0 < b1) load(b0, true);
+    char *red_at = lq_lds + Lds::R_AT;
+    do {
+        f32x4 y[RT][TT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) wb[r] = lq_transpose(w[r]);
-        if (b + WAVES < blocks) load(b + WAVES);
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int i = 0; i < GB; ++i) {
-            f32x4 acc[RT][TT], off[TT];
-            u32x4 xb[TT][GROUP / 32];
+            for (int t = 0; t < TT; ++t) y[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int b = b0; b < b1; b += STEP) {
+            const int sj = SCB > 1 ? (b - b0) % SCB : 0;  // the block's place in its piece of scales
+            if (sj == 0) put_scales();
+            put();
+            // the wave's own writes, read by its other lanes: LDS keeps their order, the compiler is told to
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            u32x4 wb[RT];
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                off[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < GROUP / 32; ++j) {
-                    xb[t][j] = *(const u32x4 *)(xget[t] + (i * (GROUP / 32) + j) * 64);
-                    off[t] = mfma_bf16(xb[t][j], offset, off[t]);
-                }
+            for (int r = 0; r < RT; ++r) wb[r] = lq_transpose(w[r]);
+            const bool same = b + STEP < b1;  // else the next tile's first block
+            if (same || (Lds::LOOP && tile + stride < tiles)) {
+                if (!same) columns(tile + stride);
+                const int nb = same ? b + STEP : b0;
+                load(nb, !same || sj == SCB - 1);
             }
 #pragma unroll
-            for (int j = 0; j < GROUP / 32; ++j)
+            for (int i = 0; i < GB; ++i) {
+                f32x4 acc[RT][TT], off[TT];
+                u32x4 xb[TT][GROUP / 32];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    off[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < GROUP / 32; ++j) {
+                        xb[t][j] = *(const u32x4 *)(xget[t] + (i * (GROUP / 32) + j) * 64);
+                        off[t] = mfma_bf16(xb[t][j], offset, off[t]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < GROUP / 32; ++j)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const u32x4 v = lq_unpack(wb[r][i * (GROUP / 32) + j]);
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) acc[r][t] = mfma_bf16(xb[t][j], v, j ? acc[r][t] : off[t]);
+                    }
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const u32x4 v = lq_unpack(wb[r][i * (GROUP / 32) + j]);
+                    const float sv = sc[(16 * r + c16) * SROW + sj * GB + i];
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[r][t] = mfma_bf16(xb[t][j], v, j ? acc[r][t] : off[t]);
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[r][t][e] = __builtin_fmaf(sv, acc[r][t][e], y[r][t][e]);
                 }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float sv = sc[(16 * r + c16) * GB + i];
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[r][t][e] = __builtin_fmaf(sv, acc[r][t][e], y[r][t][e]);
             }
         }
-    }
 
-    __syncthreads();
-    float *red = (float *)lq_lds;  // [waves][RT][TT][64 lanes][4]
+        // The waves' sums together.  In a loop the next tile's loads are under way, and its sums go to the
+        // other place: a wave is there only after all have passed this barrier once more.
+        if (!Lds::LOOP) __syncthreads();
+        float *red = (float *)red_at;  // [waves][RT][TT][64 lanes][4]
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) *(f32x4 *)(red + (((wave * RT + r) * TT + t) * 64 + lane) * 4) = y[r][t];
-    __syncthreads();
-    // one value a thread and turn: column n, token t
-    for (int i = tid; i < RT * TT * 256; i += THREADS) {
-        const int c = i & 15, t16 = (i >> 4) & 15, t = (i >> 8) % TT, r = (i >> 8) / TT;
-        const int n = n0 + 16 * r + c, tok = 16 * t + t16;
-        if (n >= a.N || tok >= tokens) continue;
-        const float *src = red + ((r * TT + t) * 64 + (t16 >> 2) * 16 + c) * 4 + (t16 & 3);
-        float v = 0.f;
+            for (int t = 0; t < TT; ++t) *(f32x4 *)(red + (((wave * RT + r) * TT + t) * 64 + lane) * 4) = y[r][t];
+        __syncthreads();
+        // one value a thread and turn: column n, token t
+        for (int i = tid; i < RT * TT * 256; i += THREADS) {
+            const int c = i & 15, t16 = (i >> 4) & 15, t = (i >> 8) % TT, r = (i >> 8) / TT;
+            const int n = tile * 16 * RT + 16 * r + c, tok = 16 * t + t16;
+            if (n >= a.N || tok >= tokens) continue;
+            const float *src = red + ((r * TT + t) * 64 + (t16 >> 2) * 16 + c) * 4 + (t16 & 3);
+            float v = 0.f;
 #pragma unroll
-        for (int u = 0; u < WAVES; ++u) v += src[u * RT * TT * 256];
-        const int64_t at = (int64_t)(tok0 + tok) * a.N + n;
-        if (a.residual) v += bf16_to_f32(a.residual[at]);
-        if (a.out_f32) ((float *)a.out)[at] = v;
-        else ((__bf16 *)a.out)[at] = (__bf16)v;
-    }
+            for (int u = 0; u < WAVES; ++u) v += src[u * RT * TT * 256];
+            const int64_t at = (int64_t)(tok0 + tok) * a.N + n;
+            if (a.residual) v += bf16_to_f32(a.residual[at]);
+            if (a.out_f32) ((float *)a.out)[at] = v;
+            else ((__bf16 *)a.out)[at] = (__bf16)v;
+        }
+        red_at = lq_lds + 2 * Lds::R_AT + Lds::R_BYTES - (red_at - lq_lds);
+        tile += stride;
+    } while (Lds::LOOP && tile < tiles);
 }
 
 size_t linear_q4_workspace(int, int, int) { return 256; }
@@ -233,13 +281,16 @@ size_t linear_q4_workspace(int, int, int) { return 256; }
 template <int GROUP, bool SB, int RT, int TR, int WAVES>
 static hipError_t linear(const LinearQ4 &a, hipStream_t st)
 {
-    constexpr int lds = LqLds<GROUP, RT, TR, WAVES>::BYTES;
+    using Lds = LqLds<GROUP, SB, RT, TR, WAVES>;
+    constexpr int lds = Lds::BYTES;
     if (lds > 64 << 10) {
         static std::atomic<uint64_t> done{0};
         const hipError_t e = allow_lds((const void *)k_linear_q4<GROUP, SB, RT, TR, WAVES>, lds, done);
         if (e != hipSuccess) return e;
     }
-    const unsigned gx = (a.N + 16 * RT - 1) / (16 * RT);
+    const int tiles = (a.N - 1) / (16 * RT) + 1;
+    const int fit = TR == 16 ? 512 : 256;  // workgroups that are resident together, by their registers
+    const unsigned gx = Lds::LOOP && tiles > fit ? fit : tiles;
     for (int64_t t0 = 0; t0 < a.T; t0 += 32768 * TR) {
         const int64_t left = (a.T - t0 + TR - 1) / TR;
         hipLaunchKernelGGL((k_linear_q4<GROUP, SB, RT, TR, WAVES>), dim3(gx, (unsigned)(left < 32768 ? left : 32768)),
@@ -252,7 +303,7 @@ template <int GROUP, bool SB>
 static hipError_t linear_tiles(const LinearQ4 &a, hipStream_t st)
 {
     // Two tiles of columns a workgroup where they still fill the chip, else one: measured at 32 x 6144 x
-    // 8192 16 us against 25, three tiles 18.8; at 1 x 1536 x 1024 (96 tiles) one is faster.  Sixteen waves
+    // 8192 15.6 us against 25, three tiles 18.8; at 1 x 1536 x 1024 (96 tiles) one is faster.  Sixteen waves
     // for a few tokens of a long K and few columns (1 x 6144 x 8192: 9.3 us, eight waves 10.3), four for
     // many columns (1 x 50257 x 2048: 15.5 us, two 20.5).  From 5 tokens on eight: sixteen leave a wave 128
     // registers, too few for 32 tokens (39 us), and 23 us at 5 x 50257 x 2048; twelve are no faster.

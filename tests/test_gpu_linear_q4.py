@@ -97,6 +97,14 @@ def test_wide():
     check(32, 5000, 1024, 128, True)
 
 
+@pytest.mark.parametrize("N,K", [(16385, 160), (50257, 96), (33000, 1152)])
+@pytest.mark.parametrize("T", [4, 5, 16, 17, 32])
+def test_many_columns(T, N, K):
+    """More tiles of columns than workgroups fit at once, the last tile short; waves with and without a block of K."""
+    check(T, N, K, 32, False)
+    check(T, N, K, 32, True)
+
+
 def test_residual_and_in_place():
     import torch
     for T in (1, 7, 32, 70):

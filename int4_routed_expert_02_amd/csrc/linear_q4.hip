@@ -21,8 +21,6 @@
 // pattern takes 10.4 us).  32 x 6144 x 8192, 26 MB in 14.4 us: every workgroup reads all
 // activations (100 MB from the L2s); without products and activations the weights take
 // 9.5 us.  1 x 1536 x 1024 takes 3 us on the device and is bound by the call.
-#include <type_traits>
-
 #include "moe_device.h"
 #include "moe_launch.h"
 

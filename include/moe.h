@@ -456,6 +456,12 @@ int moe_bias_update(int32_t E, const int32_t *counts, float *router_bias, float 
  * page id outside [0, n_pages) marks an absent page (one not there yet or
  * given back): nothing is written to it and its tokens are not seen.  The same
  * goes for an open page of a slot outside [0, n_slots).
+ * A kv_len above max_len: moe_kv_attention sees, and moe_kv_read returns, only what
+ * lies below max_len, with the values that it has under any other bound (whether a
+ * page is full goes by kv_len).  moe_kv_append stores the rows below max_len, in 8
+ * bits the rest of the page that max_len cuts too.  Rows that an append leaves out,
+ * for max_len or max_rows, have to be appended by a later call before anything reads
+ * them or, in 8 bits, another row of their page.
  * The device tables are not checked on the host; the kernels keep every access
  * inside the sizes of the shape whatever the tables hold.
  */
@@ -466,7 +472,7 @@ typedef struct {
     int32_t n_seq;       /* sequences of the batch, >= 0 */
     int32_t rows;        /* rows (new tokens) of all sequences, >= 0 */
     int32_t max_rows;    /* no sequence has more rows than this (rows beyond it are left out), 0..rows */
-    int32_t max_len;     /* no kv_len is above this (positions from it on are left out), 0..2^30 */
+    int32_t max_len;     /* no kv_len is above this (positions from it on are left out), 0..2^30; see below */
     int32_t q_heads, kv_heads; /* q head h reads key/value head h / (q_heads / kv_heads) */
     int32_t head_dim;    /* 64 or 128 */
     int32_t kv_bits;     /* 8 or 16 */

@@ -170,7 +170,11 @@ __device__ __forceinline__ void append_page(const KvArgs &a, const KvAppend &n, 
 {
     constexpr int LPR = D / 8, RPP = KVA_THREADS / LPR;  // lanes a row, rows a pass
     const KvSeq sq = kv_seq(a, s);
-    const int L = kv_limit(a, sq), start = sq.len - sq.n_pos, log2p = a.page_log2, P = 1 << log2p;
+    const int start = sq.len - sq.n_pos, log2p = a.page_log2, P = 1 << log2p;
+    // In 8 bits the page that max_len cuts is stored whole: its codes need all its rows, and who reads below
+    // max_len finds them there once the sequence is past the page.
+    const int L = BITS == 16 ? kv_limit(a, sq)
+                             : min(min(sq.len, (a.max_len + P - 1) & -P), a.max_pages << log2p);
     // this call's rows that have a place: positions [lo_all, hi_all)
     const int lo_all = max(start, 0), hi_all = min(L, start + sq.n);
     if (hi_all <= lo_all) return;
@@ -352,7 +356,7 @@ __device__ __forceinline__ void read_page(const KvArgs &a, uint16_t *out, int s,
     int64_t id = kv_page(a, s, page);
     float scale = 1.0f;
     if (BITS == 8) {
-        if (id >= 0 && ((page + 1) << log2p) > L) {  // still open
+        if (id >= 0 && (page << log2p) >= kv_full(a, sq)) {  // still open
             const int slot = kv_slot(a, s);
             if (slot >= 0) half = (IS_V ? a.v_tail : a.k_tail) + kv_block_at(a, (int64_t)slot * 2 + (page & 1), h);
             id = -1;

@@ -109,12 +109,12 @@ __device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, 
     kv_sees(a, sq, L, 0, lo, hi);
     kv_sees(a, sq, L, max(sq.n - 1, 0), lo1, hi1);
     DecTiles t;
-    t.F = a.kv_bits == 8 ? min((L >> a.page_log2) << a.page_log2, hi1) : hi1;
+    t.F = a.kv_bits == 8 ? min(kv_full(a, sq), hi1) : hi1;
     t.t0 = lo & ~63;
     t.n_codes = t.F > t.t0 ? (t.F - t.t0 + 63) >> 6 : 0;
     int n_open = 0;
     if (a.kv_bits == 8) {
-        t.F = max((L >> a.page_log2) << a.page_log2, t.t0);
+        t.F = max(kv_full(a, sq), t.t0);
         n_open = hi1 > t.F ? (hi1 - t.F + 63) >> 6 : 0;
     }
     t.total = t.n_codes + n_open;
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const RowTile tl = row_tile(a, sq, L, t, rt, TILE_ROWS);
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
-    const int F = BITS == 8 ? (L >> log2p) << log2p : 0;  // from here on: the open page
+    const int F = BITS == 8 ? kv_full(a, sq) : 0;  // from here on: the open page
     const int slot = BITS == 8 ? kv_slot(a, s) : -1;
 
     // the wave's rows, the lane's row

@@ -35,6 +35,11 @@ __device__ __forceinline__ int kv_limit(const KvArgs &a, const KvSeq &q)
     return min(min(q.len, a.max_len), a.max_pages << a.page_log2);
 }
 
+// Positions below this lie in full pages (8 bits: these have their codes, the
+// rows of the page from here on are in the sequence's open page).  That goes by
+// the sequence's length: a smaller max_len opens no page.
+__device__ __forceinline__ int kv_full(const KvArgs &a, const KvSeq &q) { return (q.len >> a.page_log2) << a.page_log2; }
+
 // The page of a sequence's position block, -1 where it is absent.
 __device__ __forceinline__ int kv_page(const KvArgs &a, int s, int block)
 {

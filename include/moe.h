@@ -446,10 +446,15 @@ int moe_bias_update(int32_t E, const int32_t *counts, float *router_bias, float 
  *               sequence's open pages, which the caller also owns:
  *               k_tail [n_slots][2][kv_heads][P][D], v_tail [n_slots][2][kv_heads][D][P],
  *               page i of the sequence in half i % 2 of its slot.  So the stored
- *               values do not depend on how the tokens were cut into appends, and
- *               the rows of the two newest pages are always there in bf16: the last
- *               P tokens can be dropped (drafted tokens that were refused) by
- *               passing a smaller kv_len.
+ *               values do not depend on how the tokens were cut into appends.  The
+ *               rows of page i stay there until a row of page i + 2 or of a later one
+ *               is appended, so tokens can be dropped (drafted ones that were refused)
+ *               by passing a smaller kv_len: any multiple of P, where no page is open,
+ *               or a length inside a page whose rows are still there.  These are all
+ *               lengths from H - P on, H the longest that the sequence has been: one
+ *               drop after another counts from the same H.  Inside an older page a
+ *               length reads other tokens' rows; go to the page's start (or another
+ *               multiple of P) and append its tokens again.
  * Row i of sequence s is row row_start[s] + i of the batch's tensors; with n_s =
  * row_start[s+1] - row_start[s] rows it has position kv_len[s] - n_s + i, kv_len
  * counting the new rows.  Position p lives in page pages[s][p / P], row p % P.  A

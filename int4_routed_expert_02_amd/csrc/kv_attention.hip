@@ -36,7 +36,7 @@
 namespace moe {
 
 constexpr float LOG2E = 1.44269504088896341f;
-constexpr float M_NONE = -1e30f;  // running maximum before any score
+constexpr float M_NONE = -0x1.fffffep127f;  // running maximum before any score: no finite score lies below it
 // The running maximum is raised only when a score passes it by more than this
 // (in powers of two): weights stay below 2^8, and most tiles skip the reduction
 // over lanes and the rescaling of the accumulator.

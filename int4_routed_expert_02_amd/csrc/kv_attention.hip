@@ -103,17 +103,17 @@ struct DecTiles {
 // Waves of a workgroup: they take a part's tiles in turn, and join their results in LDS.
 constexpr int DEC_WAVES = 8;
 
-__device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, int L, int ns)
+__device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, int L, int ns, int bits)
 {
     int lo, hi, lo1, hi1;
     kv_sees(a, sq, L, 0, lo, hi);
     kv_sees(a, sq, L, max(sq.n - 1, 0), lo1, hi1);
     DecTiles t;
-    t.F = a.kv_bits == 8 ? min(kv_full(a, sq), hi1) : hi1;
+    t.F = bits == 8 ? min(kv_full(a, sq), hi1) : hi1;
     t.t0 = lo & ~63;
     t.n_codes = t.F > t.t0 ? (t.F - t.t0 + 63) >> 6 : 0;
     int n_open = 0;
-    if (a.kv_bits == 8) {
+    if (bits == 8) {
         t.F = max(kv_full(a, sq), t.t0);
         n_open = hi1 > t.F ? (hi1 - t.F + 63) >> 6 : 0;
     }
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
     const KvSeq sq = kv_seq(a, s);
     if (sq.n == 0) return;
     const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
-    const DecTiles tl = dec_tiles(a, sq, L, t.ns);
+    const DecTiles tl = dec_tiles(a, sq, L, t.ns, BITS);
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
     const int rows = sq.n * t.group;
@@ -475,11 +475,13 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
         }
     }
     if (wave) return;
+    int group = t.group;
+    asm("" : "+s"(group));  // divided by anew: the constant of the first division would take a register through the loops
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = r16 + 16 * n;
         if (r >= rows) continue;
-        const int64_t at = (int64_t)(sq.row0 + r / t.group) * a.q_heads + kh * t.group + r % t.group;
+        const int64_t at = (int64_t)(sq.row0 + r / group) * a.q_heads + kh * group + r % group;
         if (tl.parts > 1) {
             const int64_t pt = (int64_t)split * a.rows * a.q_heads + at;
 #pragma unroll
@@ -919,7 +921,7 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     const int64_t rh = idx / (D / 4);
     const int i = (int)(rh / a.q_heads), h = (int)(rh % a.q_heads), d = (int)(idx % (D / 4)) * 4;
     if (i >= sq.n) return;
-    const int parts = few ? dec_tiles(a, sq, L, t.ns).parts
+    const int parts = few ? dec_tiles(a, sq, L, t.ns, a.kv_bits).parts
                           : row_tile(a, sq, L, t, (i * t.group + h % t.group) / (32 * tile_waves(D)), 32 * tile_waves(D)).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
@@ -970,7 +972,7 @@ __global__ __launch_bounds__(256) void k_attn_parts_few(KvArgs a, KvAttend t)
     const KvSeq sq = kv_seq(a, s);
     const int L = kv_limit(a, sq), d = threadIdx.x % LANES * 4, pl = threadIdx.x / LANES;
     if (i >= sq.n) return;
-    const int parts = dec_tiles(a, sq, L, t.ns).parts;
+    const int parts = dec_tiles(a, sq, L, t.ns, a.kv_bits).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;

@@ -41,6 +41,10 @@ constexpr float M_NONE = -0x1.fffffep127f;  // running maximum before any score:
 // (in powers of two): weights stay below 2^8, and most tiles skip the reduction
 // over lanes and the rescaling of the accumulator.
 constexpr float M_SLACK = 8.0f;
+// Where every position is seen, a weight's exponent is z c - m in one fused step: z c unrounded,
+// m a rounded one, so it may pass 0 by half of m's spacing.  Up to this size that is half a unit; in a
+// tile with a larger maximum z c is rounded first, like the m that it is compared with.
+constexpr float M_FUSED = 0x1p24f;
 
 struct KvAttend {
     const uint16_t *q;
@@ -214,12 +218,21 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
         const int j0 = b0 + 16 * g;
         float xm[NT];
         if (full) {
+            bool large = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float m = z[n][0][0];
 #pragma unroll
                 for (int i = 1; i < 16; ++i) m = fmaxf(m, z[n][i / 4][i % 4]);
                 xm[n] = m * c;
+                large |= fabsf(xm[n]) > M_FUSED;
+            }
+            if (__builtin_amdgcn_ballot_w64(large)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) z[n][u] *= c;
+                c = 1.0f;
             }
         } else {
 #pragma unroll
@@ -772,7 +785,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
             for (int T = 0; T < 2; ++T) z[T] = mfma32_bf16(*lds.k(buf, 32 * T + c32, 2 * k + h32), q[k], z[T]);
         // z[n / 2][8 (n % 2) + j]: chunk n, position b0 + 16 n + 8 h32 + j
-        const f32x4 c = lds.chunks(buf)[0];
+        f32x4 c = lds.chunks(buf)[0];
         const int care = __builtin_amdgcn_readfirstlane(*(const int *)(lds.chunks(buf) + 4));
         float xm = -INFINITY;
         auto raise = [&]() {
@@ -810,6 +823,14 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
                 for (int j = 1; j < 8; ++j) mx = fmaxf(mx, z[n >> 1][(n & 1) * 8 + j]);
                 xm = fmaxf(xm, mx * c[n]);
+            }
+            if (__builtin_amdgcn_ballot_w64(fabsf(xm) > M_FUSED)) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[n >> 1][(n & 1) * 8 + j] *= c[n];
+                    c[n] = 1.0f;
+                }
             }
             raise();
             const f32x4 lv = lds.chunks(buf)[1], iv = lds.chunks(buf)[2];

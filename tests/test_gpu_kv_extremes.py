@@ -60,3 +60,13 @@ def test_scores_far_below_zero(new, lens, dim, size, bits):
     if bits == 8:
         b.cache.k_tail.abs_()
     check_best(b, -queries(b).abs() * size, f"scores about -{size * size * dim ** 0.5:.0e}, new {new}, {bits} bits")
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dim,size", [(64, 3e3), (64, 1e5), (64, 1e12), (128, 1e9), (128, 1e18)])
+@pytest.mark.parametrize("new,lens", [([1, 1, 3], [300, 65, 700]), ([150, 40], [400, 300])], ids=["few", "many"])
+def test_scores_whose_spacing_is_large(new, lens, dim, size, bits):
+    """Tiles of 64 positions that every row sees, with scores from 1e8 to 1e37 of both signs."""
+    b = Batch(new, lens, 8, 2, dim, bits=bits, page=32, seed=32)
+    fill(b, k_std=size)
+    check_best(b, queries(b) * size, f"scores about {size * size * dim ** 0.5:.0e}, new {new}, {bits} bits")

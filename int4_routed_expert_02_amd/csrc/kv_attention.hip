@@ -37,9 +37,10 @@ namespace moe {
 
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr float M_NONE = -0x1.fffffep127f;  // running maximum before any score: no finite score lies below it
-// The running maximum is raised only when a score passes it by more than this
-// (in powers of two): weights stay below 2^8, and most tiles skip the reduction
-// over lanes and the rescaling of the accumulator.
+// The running maximum m is set this far (in powers of two) above the largest score, and
+// raised only when a score passes it: no weight is above 1, so sums pass f32's range no
+// sooner than sums of the values themselves, and most tiles skip the reduction over
+// lanes and the rescaling of the accumulator.
 constexpr float M_SLACK = 8.0f;
 // Where every position is seen, a weight's exponent is z c - m in one fused step: z c unrounded,
 // m a rounded one, so it may pass 0 by half of m's spacing.  Up to this size that is half a unit; in a
@@ -151,14 +152,14 @@ struct DecState {
     {
         bool up = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) up |= xm[n] > m[n] + M_SLACK;
+        for (int n = 0; n < NT; ++n) up |= xm[n] > m[n];
         if (!__builtin_amdgcn_ballot_w64(up)) return;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x = xm[n];
             x = fmaxf(x, __shfl_xor(x, 16, WAVE));
             x = fmaxf(x, __shfl_xor(x, 32, WAVE));
-            const float mn = fmaxf(m[n], x), f = __builtin_amdgcn_exp2f(m[n] - mn);
+            const float mn = x > m[n] ? x + M_SLACK : m[n], f = __builtin_amdgcn_exp2f(m[n] - mn);
             m[n] = mn;
             l[n] *= f;
 #pragma unroll
@@ -789,9 +790,9 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
         const int care = __builtin_amdgcn_readfirstlane(*(const int *)(lds.chunks(buf) + 4));
         float xm = -INFINITY;
         auto raise = [&]() {
-            if (!__builtin_amdgcn_ballot_w64(xm > m + M_SLACK)) return;
+            if (!__builtin_amdgcn_ballot_w64(xm > m)) return;
             xm = fmaxf(xm, __shfl_xor(xm, 32, WAVE));
-            const float mn = fmaxf(m, xm), f = __builtin_amdgcn_exp2f(m - mn);
+            const float mn = xm > m ? xm + M_SLACK : m, f = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= f;
 #pragma unroll

@@ -70,3 +70,26 @@ def test_scores_whose_spacing_is_large(new, lens, dim, size, bits):
     b = Batch(new, lens, 8, 2, dim, bits=bits, page=32, seed=32)
     fill(b, k_std=size)
     check_best(b, queries(b) * size, f"scores about {size * size * dim ** 0.5:.0e}, new {new}, {bits} bits")
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("seqs,new", [(64, 1), (64, 4), (2, 130)], ids=["few", "several", "many"])
+def test_values_near_the_largest_number(seqs, new, bits):
+    """Every 512 positions the largest score grows by 5, all values are 2e38: the weights' sum is 1.007 times the largest,
+    so nothing passes f32's range as long as no weight passes 1."""
+    import torch
+    length, dim, heads = 1600, 64, 8
+    b = Batch([length] * seqs, [length] * seqs, heads, heads, dim, bits=bits, page=64, seed=33)
+    z = np.full(length, -100.0)
+    z[5::512] = 5.0 * np.arange(len(z[5::512]))
+    k = torch.from_numpy(z / 8).to(torch.bfloat16).cuda()[None, :, None, None].expand(seqs, length, heads, dim).reshape(-1, heads, dim)
+    v = torch.full_like(k, 2e38)
+    moe.moe_kv_append(b.sh, b.batch, b.cache.handle, k.contiguous(), v)
+    c = b.sub([new] * seqs, [length] * seqs)
+    q = torch.ones(c.rows, heads, dim, dtype=torch.bfloat16, device="cuda")
+    held = stored(b, 0)[0][:, 0, 0] * 8                                            # the scores that the cache's keys give
+    best = torch.from_numpy(np.maximum.accumulate(held)[-new:]).cuda().repeat(seqs)   # the largest that each row sees
+    for f32 in (True, False):
+        out, lse = attend(c, q, f32=f32)
+        assert ((out.double() / 2e38 - 1).abs() <= 2 ** -7).all(), out.flatten()[:4]
+        assert ((lse - best[:, None]).abs() < 0.2).all()

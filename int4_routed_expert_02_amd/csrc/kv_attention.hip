@@ -94,7 +94,7 @@ __device__ __forceinline__ void kv_sees(const KvArgs &a, const KvSeq &sq, int L,
 {
     const int p = sq.len - sq.n_pos + i;
     hi = a.causal ? min(max(p + 1, 0), L) : L;
-    lo = a.window ? max(0, p - a.window + 1) : 0;
+    lo = a.window ? max(0, max(p + 1, 0) - a.window) : 0;  // the difference of two numbers from 0 on stays in 32 bits
 }
 
 // ---------------------------------------------------------------- few rows

@@ -10,7 +10,7 @@ import pytest
 import int4_routed_expert_02_amd as moe
 from gpu_util import say
 from kv_testutil import Batch, bf16_np, fill, stored
-from test_gpu_kv_attention import attend, queries
+from test_gpu_kv_attention import attend, check, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,13 @@ def test_values_near_the_largest_number(seqs, new, bits):
         out, lse = attend(c, q, f32=f32)
         assert ((out.double() / 2e38 - 1).abs() <= 2 ** -7).all(), out.flatten()[:4]
         assert ((lse - best[:, None]).abs() < 0.2).all()
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("new,lens", [([6, 1], [3, 200]), ([90, 40], [70, 40])], ids=["few", "many"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 30, 2 ** 30])
+def test_window_wider_than_any_sequence(window, new, lens, bits):
+    """It hides nothing, from rows before position 0 either (they see the whole sequence where nothing is causal)."""
+    b = Batch(new, lens, 4, 2, 64, bits=bits, page=16, window=window, flags=moe.MOE_KV_NONCAUSAL, seed=34)
+    fill(b)
+    check(b, queries(b), f"window {window}, new {new} of {lens}, {bits} bits")

@@ -572,7 +572,10 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  * moe_linear_q4 -- y = x W^T for a few tokens, W packed int4 with group scales:
  *   out[t][n] = sum over groups g of scales[n][g] * sum_{k in g} x[t][k] * code[n][k]
  *               (+ residual[t][n]),
- * products exact on the matrix cores, all sums in f32, rounded once at the end.
+ * products exact on the matrix cores, all sums in f32, rounded once at the end.  An
+ * output that the f32 sums leave infinite or NaN is taken anew in 64 bits, so infinite
+ * activations and the largest finite ones give what the formula gives (such calls
+ * take longer).
  *   x         [T][K] bf16, row stride x_row_stride elements
  *   q         [N][K/2] bytes, codes packed as everywhere in this file: what
  *             moe_quantize_rows(rows = N * K / group, cols = group, bits 4) writes

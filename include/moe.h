@@ -474,11 +474,11 @@ int moe_bias_update(int32_t E, const int32_t *counts, float *router_bias, float 
 #define MOE_KV_ROPE_PAIRS 0x20000u /* moe_kv_append: rotate adjacent pairs (2j, 2j+1); otherwise (j, j + rot_dim/2) */
 
 typedef struct {
-    int32_t n_seq;       /* sequences of the batch, >= 0 */
-    int32_t rows;        /* rows (new tokens) of all sequences, >= 0 */
+    int32_t n_seq;       /* sequences of the batch, >= 0; n_seq * kv_heads below 2^26 */
+    int32_t rows;        /* rows (new tokens) of all sequences, >= 0; rows * q_heads below 2^26 */
     int32_t max_rows;    /* no sequence has more rows than this (rows beyond it are left out), 0..rows */
     int32_t max_len;     /* no kv_len is above this (positions from it on are left out), 0..2^30; see below */
-    int32_t q_heads, kv_heads; /* q head h reads key/value head h / (q_heads / kv_heads) */
+    int32_t q_heads, kv_heads; /* q head h reads key/value head h / (q_heads / kv_heads); at most 2^22 */
     int32_t head_dim;    /* 64 or 128 */
     int32_t kv_bits;     /* 8 or 16 */
     int32_t page_tokens; /* 16, 32, 64 or 128 */

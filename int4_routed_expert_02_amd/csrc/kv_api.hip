@@ -20,6 +20,7 @@ int check_shape(const moe_kv_shape *s)
     if (s->kv_bits == 8 && s->n_slots < 0) return MOE_ERR_SHAPE;
     if (!(s->scale - s->scale == 0.0f)) return MOE_ERR_SHAPE;  // infinite or NaN
     if ((int64_t)s->max_pages * s->page_tokens > 1 << 30 || s->max_len > 1 << 30) return MOE_ERR_SHAPE;
+    if (s->q_heads > 1 << 22) return MOE_ERR_SHAPE;
     if ((int64_t)s->rows * s->q_heads > INT32_MAX / 32 || (int64_t)s->n_seq * s->kv_heads > INT32_MAX / 32)
         return MOE_ERR_SHAPE;
     // what the gfx950 kernels cover

@@ -27,6 +27,11 @@ namespace moe {
 
 constexpr int KVA_THREADS = 256;
 
+// A launch's workgroups: for pages, for each sequence's queries, all of them; and the pages of a sequence.
+struct KvaGroups {
+    int pages, queries, all, touched;
+};
+
 __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi)
 {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -164,7 +169,7 @@ __device__ __forceinline__ void store_transposed(uint16_t *dst, int log2p, PageT
     }
 }
 
-template <int D, int BITS, bool IS_V>
+template <int D, int BITS, bool EVEN, bool IS_V>
 __device__ __forceinline__ void append_page(const KvArgs &a, const KvAppend &n, int s, int t, int h, uint16_t *lds,
                                             uint32_t *red)
 {
@@ -177,9 +182,9 @@ __device__ __forceinline__ void append_page(const KvArgs &a, const KvAppend &n, 
                              : min(min(sq.len, (a.max_len + P - 1) & -P), a.max_pages << log2p);
     // this call's rows that have a place: positions [lo_all, hi_all)
     const int lo_all = max(start, 0), hi_all = min(L, start + sq.n);
-    if (hi_all <= lo_all) return;
+    if ((!EVEN && t < 0) || hi_all <= lo_all) return;
     const int first = lo_all >> log2p, last = (hi_all - 1) >> log2p, page = first + t;
-    if (page > last) return;
+    if (EVEN ? page > last : t > last - first) return;
     const int id = kv_page(a, s, page), slot = BITS == 8 ? kv_slot(a, s) : -1;
     const PageTile<D> tile{lds};
     const int lane_row = threadIdx.x / LPR, e = (threadIdx.x % LPR) * 8;
@@ -310,32 +315,48 @@ __device__ __forceinline__ void append_page(const KvArgs &a, const KvAppend &n, 
     }
 }
 
-template <int D, int BITS>
-__global__ __launch_bounds__(KVA_THREADS) void k_kv_append(KvArgs a, KvAppend n, int touched, int page_groups,
-                                                           int q_groups)
+// The sequence and touched page of the b-th unit: `touched` pages of every sequence, or as many as the rows of
+// each can touch.
+template <bool EVEN>
+__device__ __forceinline__ int page_unit(const KvArgs &a, int b, int touched, int &t)
+{
+    if (!EVEN) return kv_unit(a, b, 1, a.page_log2, 2, t);
+    t = b % touched;
+    return b / touched;
+}
+
+template <int D, int BITS, bool EVEN>
+__global__ __launch_bounds__(KVA_THREADS) void k_kv_append(KvArgs a, KvAppend n, KvaGroups g)
 {
     extern __shared__ __align__(16) uint16_t kva_tile[];
     __shared__ uint32_t red[KVA_THREADS / WAVE];
-    int b = blockIdx.x;
-    if (b < page_groups) {
+    int b = EVEN ? (int)blockIdx.x : kv_block();
+    if (b < g.pages) {
         const int is_v = b & 1;
         b >>= 1;
         const int h = b % a.kv_heads;
-        b /= a.kv_heads;
-        const int t = b % touched, s = b / touched;
-        if (is_v) append_page<D, BITS, true>(a, n, s, t, h, kva_tile, red);
-        else append_page<D, BITS, false>(a, n, s, t, h, kva_tile, red);
+        int t;
+        const int s = page_unit<EVEN>(a, b / a.kv_heads, g.touched, t);
+        if (is_v) append_page<D, BITS, EVEN, true>(a, n, s, t, h, kva_tile, red);
+        else append_page<D, BITS, EVEN, false>(a, n, s, t, h, kva_tile, red);
         return;
     }
-    // queries: q_groups workgroups a sequence
-    b -= page_groups;
-    const int s = b / q_groups;
-    const KvSeq sq = kv_seq(a, s);
-    const int64_t i = (int64_t)(b % q_groups) * KVA_THREADS + threadIdx.x;
+    if (!EVEN && b >= g.all) return;
+    // queries: g.queries workgroups a sequence, or all rows of the batch one after another
+    b -= g.pages;
+    int s = 0;
+    if (EVEN) {
+        s = b / g.queries;
+        b %= g.queries;
+    }
+    const int64_t i = (int64_t)b * KVA_THREADS + threadIdx.x;
     const int64_t head_row = i / (D / 8);
     const int e = (int)(i % (D / 8)) * 8;
-    const int r = (int)(head_row / a.q_heads), h = (int)(head_row % a.q_heads);
-    if (r >= sq.n) return;  // the lanes of a row leave together
+    int r = (int)(head_row / a.q_heads);
+    const int h = (int)(head_row % a.q_heads);
+    if (!EVEN) s = kv_unit(a, r, 1, 0, 0, r);
+    const KvSeq sq = kv_seq(a, s);
+    if (r < 0 || r >= sq.n) return;  // the lanes of a row leave together
     const int row = sq.row0 + r, p = sq.len - sq.n_pos + r;
     const u32x4 v = normed_rotated<D>(n.q + row * n.q_stride + h * D, e, n.q_norm, n, n.pos ? n.pos[row] : p);
     *(u32x4 *)(n.q_out + ((int64_t)row * a.q_heads + h) * D + e) = v;
@@ -343,12 +364,13 @@ __global__ __launch_bounds__(KVA_THREADS) void k_kv_append(KvArgs a, KvAppend n,
 
 // ---------------------------------------------------------------- read
 
-template <int D, int BITS, bool IS_V>
+template <int D, int BITS, bool EVEN, bool IS_V>
 __device__ __forceinline__ void read_page(const KvArgs &a, uint16_t *out, int s, int t, int h, uint16_t *lds)
 {
     const KvSeq sq = kv_seq(a, s);
     const int L = kv_limit(a, sq), start = sq.len - sq.n_pos, log2p = a.page_log2, P = 1 << log2p;
     // the first touched page is the one of the first row with a position (rows before it read as 0)
+    if (!EVEN && (unsigned)t > (unsigned)(((sq.n - 1) >> log2p) + 1)) return;
     const int first = max(start, 0) >> log2p, page = first + t;
     const int lo = max(t == 0 ? start : (page << log2p), start), hi = min((page + 1) << log2p, start + sq.n);
     if (hi <= lo) return;
@@ -405,22 +427,39 @@ __device__ __forceinline__ void read_page(const KvArgs &a, uint16_t *out, int s,
     }
 }
 
-template <int D, int BITS>
-__global__ __launch_bounds__(KVA_THREADS) void k_kv_read(KvArgs a, uint16_t *k, uint16_t *v, int touched)
+template <int D, int BITS, bool EVEN>
+__global__ __launch_bounds__(KVA_THREADS) void k_kv_read(KvArgs a, uint16_t *k, uint16_t *v, KvaGroups g)
 {
     extern __shared__ __align__(16) uint16_t kva_tile[];
-    int b = blockIdx.x;
+    int b = EVEN ? (int)blockIdx.x : kv_block();
+    if (!EVEN && b >= g.all) return;
     const int is_v = b & 1;
     b >>= 1;
     const int h = b % a.kv_heads;
-    b /= a.kv_heads;
-    const int t = b % touched, s = b / touched;
-    if (is_v) read_page<D, BITS, true>(a, v, s, t, h, kva_tile);
-    else read_page<D, BITS, false>(a, k, s, t, h, kva_tile);
+    int t;
+    const int s = page_unit<EVEN>(a, b / a.kv_heads, g.touched, t);
+    if (is_v) read_page<D, BITS, EVEN, true>(a, v, s, t, h, kva_tile);
+    else read_page<D, BITS, EVEN, false>(a, k, s, t, h, kva_tile);
 }
 
-// Pages that max_rows rows can touch, wherever they start.
-static int touched_pages(const KvArgs &a) { return ((a.max_rows - 2) >> a.page_log2) + 2; }
+// Workgroups are laid out evenly, as many for each sequence as the longest may need (pages that max_rows rows can touch
+// wherever they start, and query rows), or by the sequences' own rows, which costs a search in row_start.  Evenly
+// unless that makes more than twice as many and a thousand more (6 sequences of 876 to 1501 rows, bf16: 69 us
+// evenly, 100 by rows; 32 of one row: 6.8, 7.5; one of 512 rows and 31 of one: 9.0, 8.1; one of 8192 rows and 63 of
+// one: 1260, 153), so their number goes by the rows whatever max_rows is.
+static bool groups_of(const KvArgs &a, bool queries, KvaGroups &g)
+{
+    const int64_t heads = (int64_t)a.kv_heads * 2, row = queries ? (int64_t)a.q_heads * (a.head_dim / 8) : 0;
+    g.touched = ((a.max_rows - 2) >> a.page_log2) + 2;
+    const int64_t each = (a.max_rows * row + KVA_THREADS - 1) / KVA_THREADS, pages = a.n_seq * heads * g.touched;
+    const int64_t own_pages = ((a.rows >> a.page_log2) + 2 * (int64_t)a.n_seq) * heads;
+    const int64_t own = own_pages + (a.rows * row + KVA_THREADS - 1) / KVA_THREADS;
+    const bool even = pages + each * a.n_seq <= 2 * own + 1024 && pages + each * a.n_seq <= KV_GRID_X;
+    g.pages = (int)(even ? pages : own_pages);
+    g.queries = (int)(even ? each : 0);
+    g.all = (int)(even ? pages + each * a.n_seq : own);
+    return even;
+}
 
 template <int D>
 static size_t tile_bytes(const KvArgs &a) { return ((size_t)PageTile<D>::ROW << a.page_log2) * 2; }
@@ -428,12 +467,11 @@ static size_t tile_bytes(const KvArgs &a) { return ((size_t)PageTile<D>::ROW << 
 template <int D, int BITS>
 static hipError_t append(const KvArgs &a, const KvAppend &n, hipStream_t st)
 {
-    const int touched = touched_pages(a);
-    const int64_t pages = (int64_t)a.n_seq * touched * a.kv_heads * 2;
-    const int64_t q_groups = n.q ? ((int64_t)a.max_rows * a.q_heads * (D / 8) + KVA_THREADS - 1) / KVA_THREADS : 0;
-    if (pages + q_groups * a.n_seq > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_kv_append<D, BITS>), dim3((unsigned)(pages + q_groups * a.n_seq)), dim3(KVA_THREADS),
-                       tile_bytes<D>(a), st, a, n, touched, (int)pages, (int)q_groups);
+    KvaGroups g;
+    if (groups_of(a, n.q, g))
+        hipLaunchKernelGGL((k_kv_append<D, BITS, true>), kv_grid(g.all), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, n, g);
+    else
+        hipLaunchKernelGGL((k_kv_append<D, BITS, false>), kv_grid(g.all), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, n, g);
     return hipGetLastError();
 }
 
@@ -446,11 +484,11 @@ hipError_t launch_kv_append(const KvArgs &a, const KvAppend &n, hipStream_t st)
 template <int D, int BITS>
 static hipError_t read(const KvArgs &a, uint16_t *k, uint16_t *v, hipStream_t st)
 {
-    const int touched = touched_pages(a);
-    const int64_t pages = (int64_t)a.n_seq * touched * a.kv_heads * 2;
-    if (pages > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_kv_read<D, BITS>), dim3((unsigned)pages), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, k, v,
-                       touched);
+    KvaGroups g;
+    if (groups_of(a, false, g))
+        hipLaunchKernelGGL((k_kv_read<D, BITS, true>), kv_grid(g.all), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, k, v, g);
+    else
+        hipLaunchKernelGGL((k_kv_read<D, BITS, false>), kv_grid(g.all), dim3(KVA_THREADS), tile_bytes<D>(a), st, a, k, v, g);
     return hipGetLastError();
 }
 

@@ -598,7 +598,7 @@ struct TileLds {
 };
 
 template <int D, int BITS>
-__global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles)
+__global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles, int units)
 {
     constexpr int QS = D / 16, DT = D / 32;     // contraction steps of a score, d tiles
     constexpr int TW = tile_waves(D), TILE_ROWS = 32 * TW, THREADS = TW * WAVE;
@@ -617,9 +617,15 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     b /= a.kv_heads;
     const int split = b % t.ns;
     b /= t.ns;
-    const bool by_length = a.max_len / 2 >= a.max_rows;
-    const int s = kv_ranked(a, by_length ? b / row_tiles : b % a.n_seq, lane);
-    const int rt = row_tiles - 1 - (by_length ? b % row_tiles : b / a.n_seq);
+    int s, rt;
+    if (units) {  // the sequences' row tiles one after another (ns is 1)
+        s = kv_unit(a, b, t.group, __builtin_ctz(TILE_ROWS), 1, rt);
+        if ((unsigned)rt >= (unsigned)row_tiles) return;
+    } else {
+        const bool by_length = a.max_len / 2 >= a.max_rows;
+        s = kv_ranked(a, by_length ? b / row_tiles : b % a.n_seq, lane);
+        rt = row_tiles - 1 - (by_length ? b % row_tiles : b / a.n_seq);
+    }
     const KvSeq sq = kv_seq(a, s);
     const int rows = sq.n * t.group;
     if (rt * TILE_ROWS >= rows) return;
@@ -1085,19 +1091,27 @@ static hipError_t attend_few(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
     const size_t lds = (2 * DEC_WAVES * 16 * NT + (DEC_WAVES / 2) * (D / 16) * 64 * 4) * sizeof(float);
     const int64_t grid = (int64_t)a.n_seq * a.kv_heads * t.ns;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_attn_dec<D, BITS, NT>), dim3((unsigned)grid), dim3(DEC_WAVES * WAVE), lds, st, a, t);
     return hipGetLastError();
 }
 
 template <int D, int BITS>
-static hipError_t attend_many(const KvArgs &a, const KvAttend &t, unsigned grid, int tiles, hipStream_t st)
+static hipError_t attend_many(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
+    // Row tiles are laid out evenly, for each sequence as many as the longest may have, as long as that fits one
+    // dimension of a launch; else by the sequences' own rows, with a search for a tile's sequence.
+    const int64_t tiles = row_tiles_of(a);
+    int64_t grid = tiles * a.n_seq * a.kv_heads * t.ns, units = 0;
+    if (grid > KV_GRID_X) {  // below 2^19 for the rows and 2^22 for the sequences
+        units = ((int64_t)a.rows * t.group) / (32 * tile_waves(D)) + a.n_seq;
+        grid = units * a.kv_heads;
+    }
     constexpr size_t lds = 2 * TileLds<D>::BYTES;
     static std::atomic<uint64_t> done{0};
     const hipError_t e = lds > 64 << 10 ? allow_lds((const void *)k_attn_tile<D, BITS>, (int)lds, done) : hipSuccess;
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3(grid), dim3(tile_waves(D) * WAVE), lds, st, a, t, tiles);
+    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3((unsigned)grid), dim3(tile_waves(D) * WAVE), lds, st, a, t, (int)tiles,
+                       (int)units);
     return hipGetLastError();
 }
 
@@ -1109,9 +1123,7 @@ static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
     if (few_rows(a)) {
         e = rows <= 16 ? attend_few<D, BITS, 1>(a, t, st) : attend_few<D, BITS, 2>(a, t, st);
     } else {
-        const int64_t tiles = row_tiles_of(a), grid = tiles * a.n_seq * a.kv_heads * t.ns;
-        if (grid > INT32_MAX) return hipErrorInvalidValue;
-        e = attend_many<D, BITS>(a, t, (unsigned)grid, (int)tiles, st);
+        e = attend_many<D, BITS>(a, t, st);
     }
     if (e != hipSuccess || t.ns == 1) return e;
     // More than one round of loads for a lane that takes all parts, so the parts go over lanes (one
@@ -1141,8 +1153,26 @@ hipError_t launch_kv_attention(const KvArgs &args, const uint16_t *q, int64_t q_
     t.part = (float *)ws;
     t.ns = parts_of(args);
     t.group = a.q_heads / a.kv_heads;
-    if (a.head_dim == 64) return a.kv_bits == 8 ? attend<64, 8>(a, t, st) : attend<64, 16>(a, t, st);
-    return a.kv_bits == 8 ? attend<128, 8>(a, t, st) : attend<128, 16>(a, t, st);
+    // at most as many sequences together as one dimension of a launch holds (more than that are never cut into parts)
+    const int together = (int)(KV_GRID_X / a.kv_heads);
+    for (int s0 = 0; s0 < args.n_seq; s0 += together) {
+        a.n_seq = args.n_seq - s0 < together ? args.n_seq - s0 : together;
+        a.row_start = args.row_start + s0;
+        a.kv_len = args.kv_len + s0;
+        a.pages = args.pages + (int64_t)s0 * a.max_pages;
+        if (args.slots) {
+            a.slots = args.slots + s0;
+        } else if (s0 && a.n_slots) {  // sequence s has slot s
+            const int64_t first = s0 < args.n_slots ? s0 : args.n_slots;
+            a.n_slots = args.n_slots - (int)first;
+            a.k_tail = args.k_tail + (first * 2 * a.kv_heads * a.head_dim << a.page_log2);
+            a.v_tail = args.v_tail + (first * 2 * a.kv_heads * a.head_dim << a.page_log2);
+        }
+        const hipError_t e = a.head_dim == 64 ? a.kv_bits == 8 ? attend<64, 8>(a, t, st) : attend<64, 16>(a, t, st)
+                                              : a.kv_bits == 8 ? attend<128, 8>(a, t, st) : attend<128, 16>(a, t, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe

@@ -35,6 +35,26 @@ __device__ __forceinline__ int kv_limit(const KvArgs &a, const KvSeq &q)
     return min(min(q.len, a.max_len), a.max_pages << a.page_log2);
 }
 
+// The workgroup's number in a launch of kv_grid().
+__device__ __forceinline__ int kv_block() { return (int)blockIdx.x + (int)blockIdx.y * (int)KV_GRID_X; }
+
+// Units of 2^log2 rows of `heads` heads, counted through the batch: sequence s has them
+// from (row_start[s] * heads >> log2) + extra * s on, so `extra` more than its rows fill
+// for each sequence.  Of unit u: the last sequence that begins at or below it, and the
+// unit's number in that sequence (below 0 before the first; the callers bound it above).
+__device__ __forceinline__ int kv_unit(const KvArgs &a, int u, int heads, int log2, int extra, int &t)
+{
+    auto begin = [&](int s) { return (min(max(a.row_start[s], 0), a.rows) * heads >> log2) + extra * s; };
+    int lo = 0, hi = a.n_seq;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (begin(mid) <= u) lo = mid;
+        else hi = mid;
+    }
+    t = u - begin(lo);
+    return lo;
+}
+
 // Positions below this lie in full pages (8 bits: these have their codes, the
 // rows of the page from here on are in the sequence's open page).  That goes by
 // the sequence's length: a smaller max_len opens no page.

@@ -135,6 +135,13 @@ struct KvArgs {
     float *k_scale, *v_scale;
     uint16_t *k_tail, *v_tail;
 };
+// How a launch's workgroups are laid out: a dimension of a launch holds fewer than 2^32 lanes, and more
+// than that are dropped without an error, so many workgroups are folded into rows of 2^22.
+constexpr int64_t KV_GRID_X = 1 << 22;
+inline dim3 kv_grid(int64_t groups)
+{
+    return groups <= KV_GRID_X ? dim3((unsigned)groups) : dim3((unsigned)KV_GRID_X, (unsigned)((groups + KV_GRID_X - 1) / KV_GRID_X));
+}
 struct KvAppend {
     const uint16_t *k, *v, *q;
     int64_t k_stride, v_stride, q_stride;

@@ -145,7 +145,7 @@ __device__ __forceinline__ float lq_defined(const LinearQ4 &a, int token, int n)
 
 // 16 * RT columns at a time, up to TR tokens; the workgroup's waves share out the blocks of K.
 template <int GROUP, bool SB, int RT, int TR, int WAVES>
-__global__ __launch_bounds__(WAVES *WAVE, TR <= 16 ? 4 : 2) void k_linear_q4(LinearQ4 a, int t0)
+__global__ __launch_bounds__(WAVES *WAVE, TR <= 16 ? 4 : 2) void k_linear_q4(LinearQ4 a, int t0, int tile0)
 {
     using Lds = LqLds<GROUP, SB, RT, TR, WAVES>;
     constexpr int TT = Lds::TT, GB = Lds::GB, THREADS = WAVES * WAVE, XU = TR / 4, SS = SB ? 2 : 4;
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(WAVES *WAVE, TR <= 16 ? 4 : 2) void k_linear_q4(Lin
     const int b0 = Lds::RUNS ? wave * per : wave, b1 = Lds::RUNS ? min(blocks, b0 + per) : blocks;
     constexpr int STEP = Lds::RUNS ? 1 : WAVES;
     const int stride = gridDim.x;
-    int tile = blockIdx.x;
+    int tile = tile0 + blockIdx.x;
     columns(tile);
     if (b0 < b1) load(b0, true);
     char *red_at = lq_lds + Lds::R_AT;
@@ -337,11 +337,15 @@ static hipError_t linear(const LinearQ4 &a, hipStream_t st)
     }
     const int tiles = (a.N - 1) / (16 * RT) + 1;
     const int fit = TR == 16 ? 512 : 256;  // workgroups that are resident together, by their registers
-    const unsigned gx = Lds::LOOP && tiles > fit ? fit : tiles;
+    constexpr int most = 1 << 21;  // workgroups in one dimension: it holds fewer than 2^32 lanes
     for (int64_t t0 = 0; t0 < a.T; t0 += 32768 * TR) {
         const int64_t left = (a.T - t0 + TR - 1) / TR;
-        hipLaunchKernelGGL((k_linear_q4<GROUP, SB, RT, TR, WAVES>), dim3(gx, (unsigned)(left < 32768 ? left : 32768)),
-                           dim3(WAVES * WAVE), lds, st, a, (int)t0);
+        for (int tile0 = 0; tile0 < tiles; tile0 += Lds::LOOP ? tiles : most) {
+            const int gx = tiles - tile0 < (Lds::LOOP ? fit : most) ? tiles - tile0 : Lds::LOOP ? fit : most;
+            hipLaunchKernelGGL((k_linear_q4<GROUP, SB, RT, TR, WAVES>),
+                               dim3((unsigned)gx, (unsigned)(left < 32768 ? left : 32768)), dim3(WAVES * WAVE), lds, st, a,
+                               (int)t0, tile0);
+        }
     }
     return hipGetLastError();
 }

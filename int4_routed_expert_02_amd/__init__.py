@@ -204,9 +204,13 @@ def _bind_torch():
     global _torch, _current
     import torch
     _torch = torch
-    get_device, raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    # a tenth of a microsecond; torch.cuda.current_stream() builds an object, 3 us
-    _current = lambda: raw_stream(get_device())  # noqa: E731
+    get_device = getattr(torch._C, "_cuda_getDevice", None)
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if get_device is not None and raw_stream is not None:
+        # a tenth of a microsecond; torch.cuda.current_stream() builds an object, 3 us
+        _current = lambda: raw_stream(get_device())  # noqa: E731
+    else:
+        _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     return torch
 
 

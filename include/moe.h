@@ -519,8 +519,8 @@ typedef struct {
  *         rotated by its position ((a, b) -> (a cos - b sin, a sin + b cos), computed
  *         in f32), rounded to bf16 and stored; v is stored as it is
  *   q     nullable, [rows][q_heads][head_dim] bf16, row stride q_row_stride: normed and
- *         rotated like k into q_out [rows][q_heads][head_dim], which may be q itself (its
- *         rows q_heads * head_dim apart)
+ *         rotated like k into q_out [rows][q_heads][head_dim], which may be q itself if its
+ *         rows are q_heads * head_dim apart (else MOE_ERR_SHAPE) and may not overlap it otherwise
  *   rot   nullable: no norm and no rotation
  * Different sequences of a call must not share a page that the call writes, or a slot.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (head_dim, page_tokens or

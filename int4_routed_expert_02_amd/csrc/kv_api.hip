@@ -114,6 +114,8 @@ extern "C" int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batc
         if (const int r = check_rows(q, q_row_stride, shape->q_heads, shape->head_dim)) return r;
         if (!q_out) return MOE_ERR_NULL;
         if (!aligned(q_out, 16)) return MOE_ERR_ALIGN;
+        // in place only where a row's result lies where the row was: else it would meet rows not read yet
+        if (q_out == q && shape->rows > 1 && q_row_stride != (int64_t)shape->q_heads * shape->head_dim) return MOE_ERR_SHAPE;
     }
     moe::KvAppend n = {};
     if (rot) {

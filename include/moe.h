@@ -582,13 +582,14 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  *   scales    [N][K/group] f32 (MOE_SRC_F32: that call's scales) or bf16 (MOE_SRC_BF16)
  *   residual  nullable, [T][N] bf16; may be out itself when out is bf16
  *   out       [T][N] bf16, or f32 with flags & MOE_OUT_F32
- *   ws        moe_linear_q4_workspace_bytes(T, N, K) bytes, 256-byte aligned
+ *   ws        moe_linear_q4_workspace_bytes(T, N, K) bytes, 256-byte aligned; reserved: it is
+ *             checked like every workspace, but no kernel uses it so far
  * group is 32, 64 or 128 and divides K; any N and T (made for T <= 64: a larger batch
  * reads the weights again for every 64 tokens).
  * Errors: MOE_ERR_SHAPE (negative sizes, K % group, a format or stride out of range),
- * MOE_ERR_UNSUPPORTED (group, K above 2^26, x_row_stride above 2^25), MOE_ERR_NULL, MOE_ERR_ALIGN (x, q, scales, ws; residual and
- * out to their elements; x_row_stride % 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or
- * N == 0 is a no-op.
+ * MOE_ERR_UNSUPPORTED (group; x_row_stride, and so K, above 2^25), MOE_ERR_NULL,
+ * MOE_ERR_ALIGN (x, q, scales, ws; residual and out to their elements; x_row_stride %
+ * 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or N == 0 is a no-op.
  */
 int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, const moe_bf16 *x, int64_t x_row_stride,
                   const void *q, const void *scales, int32_t scale_format, const moe_bf16 *residual, void *out,

@@ -180,9 +180,7 @@ extern "C" int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch,
 
 extern "C" size_t moe_linear_q4_workspace_bytes(int32_t T, int32_t N, int32_t K)
 {
-    if (T < 0 || N < 0 || K <= 0) return 0;
-    const size_t n = moe::linear_q4_workspace(T, N, K);
-    return n < 256 ? 256 : (n + 255) / 256 * 256;
+    return T < 0 || N < 0 || K <= 0 ? 0 : 256;  // reserved: no kernel uses it
 }
 
 extern "C" int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, const moe_bf16 *x, int64_t x_row_stride,
@@ -193,7 +191,7 @@ extern "C" int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, con
     if (scale_format != MOE_SRC_F32 && scale_format != MOE_SRC_BF16) return MOE_ERR_SHAPE;
     if ((int64_t)T * N > ((int64_t)1 << 40)) return MOE_ERR_SHAPE;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
-    if (K > 1 << 26 || x_row_stride > 1 << 25) return MOE_ERR_UNSUPPORTED;  // 32-bit offsets inside a workgroup
+    if (x_row_stride > 1 << 25) return MOE_ERR_UNSUPPORTED;  // 32-bit offsets inside a workgroup (K is no larger)
     if (T == 0 || N == 0) return MOE_OK;
     if (!x || !q || !scales || !out) return MOE_ERR_NULL;
     if (!aligned(x, 16) || x_row_stride % 8 || !aligned(q, 16) || !aligned(scales, 16)) return MOE_ERR_ALIGN;
@@ -214,6 +212,5 @@ extern "C" int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, con
     a.residual = residual;
     a.out = out;
     a.out_f32 = (flags & MOE_OUT_F32) ? 1 : 0;
-    a.ws = ws;
     return hip_status(moe::launch_linear_q4(a, (hipStream_t)stream));
 }

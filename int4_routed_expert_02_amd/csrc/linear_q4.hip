@@ -323,8 +323,6 @@ __global__ __launch_bounds__(WAVES *WAVE, TR <= 16 ? 4 : 2) void k_linear_q4(Lin
     } while (Lds::LOOP && tile < tiles);
 }
 
-size_t linear_q4_workspace(int, int, int) { return 256; }
-
 template <int GROUP, bool SB, int RT, int TR, int WAVES>
 static hipError_t linear(const LinearQ4 &a, hipStream_t st)
 {

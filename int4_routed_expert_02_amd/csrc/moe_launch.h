@@ -168,9 +168,7 @@ struct LinearQ4 {
     const uint16_t *residual;
     void *out;
     int out_f32;
-    void *ws;
 };
-size_t linear_q4_workspace(int T, int N, int K);
 hipError_t launch_linear_q4(const LinearQ4 &a, hipStream_t st);
 
 }  // namespace moe

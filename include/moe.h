@@ -548,6 +548,9 @@ int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batch, const mo
  *   out  [rows][q_heads][head_dim] bf16, or f32 with MOE_OUT_F32
  *   lse  nullable, [rows][q_heads] f32 (natural log)
  * out and lse must not overlap q.  Rows that belong to no sequence are left as they are.
+ * max_rows chooses the kernel (few or many rows of a key/value head) for the whole call: a
+ * long chunk and many single rows are faster in two calls, whose values are the same to
+ * the stated precision.
  *   ws   moe_kv_workspace_bytes(shape) bytes, 256-byte aligned (parts of a long sequence)
  * Errors as moe_kv_append, and MOE_ERR_WORKSPACE.
  */
@@ -586,10 +589,10 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  *             checked like every workspace, but no kernel uses it so far
  * group is 32, 64 or 128 and divides K; any N and T (made for T <= 64: a larger batch
  * reads the weights again for every 64 tokens).
- * Errors: MOE_ERR_SHAPE (negative sizes, K % group, a format or stride out of range),
- * MOE_ERR_UNSUPPORTED (group; x_row_stride, and so K, above 2^25), MOE_ERR_NULL,
- * MOE_ERR_ALIGN (x, q, scales, ws; residual and out to their elements; x_row_stride %
- * 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or N == 0 is a no-op.
+ * Errors: MOE_ERR_SHAPE (negative sizes, K % group, a format or stride out of range, T * N
+ * above 2^40), MOE_ERR_UNSUPPORTED (group; x_row_stride, and so K, above 2^25),
+ * MOE_ERR_NULL, MOE_ERR_ALIGN (x, q, scales, ws; residual and out to their elements;
+ * x_row_stride % 8), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or N == 0 is a no-op.
  */
 int moe_linear_q4(int32_t T, int32_t N, int32_t K, int32_t group, const moe_bf16 *x, int64_t x_row_stride,
                   const void *q, const void *scales, int32_t scale_format, const moe_bf16 *residual, void *out,

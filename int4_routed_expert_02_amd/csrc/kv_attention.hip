@@ -539,8 +539,8 @@ __device__ __forceinline__ int kv_ranked(const KvArgs &a, int r, int lane)
 }
 
 // Waves of a workgroup, 32 query rows each.
-// With heads of 128 eight share a tile's staging (2048 and 1659 rows over 16384 and 8465 positions: 1049 us,
-// four 1127); with heads of 64 four leave two workgroups a compute unit (a prompt of 4096 rows: 88 us, eight 120).
+// With heads of 128 eight share a tile's staging (2048 and 1659 rows over 16384 and 8465 positions: 1024 us,
+// four 1109); with heads of 64 four leave two workgroups a compute unit (a prompt of 4096 rows: 88 us, eight 122).
 constexpr int tile_waves(int dim) { return dim == 64 ? 4 : 8; }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -610,8 +610,8 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h32 = lane >> 5, c32 = lane & 31;
     // kv head fastest (a head's workgroups share an L2), then the longest rows first: where most positions
     // are cached ones, a long sequence's rows before a shorter one's (2048 and 1659 rows over 16384 and
-    // 8465 positions: 1009 us, 1250 with the sequences in turn), else the last rows of every sequence (3 x 1000
-    // rows: 32 us, 36 by sequences)
+    // 8465 positions: 1024 us, 1264 with the sequences in turn), else the last rows of every sequence (3 x 1000
+    // rows: 31 us, 36 by sequences)
     int b = blockIdx.x;
     const int kh = b % a.kv_heads;
     b /= a.kv_heads;

@@ -18,8 +18,8 @@
 // scale (times 16) joins a group's sum in f32.  Where that leaves f32's range the
 // output is infinite or NaN and is taken from the definition instead (lq_defined).
 //
-// What it reaches: 5 x 50257 x 2048, 58 MB in 14.7 us, 4.0 TB/s (reading alone in this
-// pattern takes 10.4 us).  32 x 6144 x 8192, 26 MB in 14.4 us: every workgroup reads all
+// What it reaches: 5 x 50257 x 2048, 58 MB in 14.9 us, 3.9 TB/s (reading alone in this
+// pattern takes 10.4 us).  32 x 6144 x 8192, 26 MB in 14.7 us: every workgroup reads all
 // activations (100 MB from the L2s); without products and activations the weights take
 // 9.5 us.  1 x 1536 x 1024 takes 3 us on the device and is bound by the call.
 #include "moe_device.h"
@@ -351,12 +351,14 @@ static hipError_t linear(const LinearQ4 &a, hipStream_t st)
 template <int GROUP, bool SB>
 static hipError_t linear_tiles(const LinearQ4 &a, hipStream_t st)
 {
-    // Two tiles of columns a workgroup where they still fill the chip, else one: measured at 32 x 6144 x
-    // 8192 15.6 us against 25, three tiles 18.8; at 1 x 1536 x 1024 (96 tiles) one is faster.  Sixteen waves
-    // for a few tokens of a long K and few columns (1 x 6144 x 8192: 9.3 us, eight waves 10.3), four for
-    // many columns (1 x 50257 x 2048: 15.5 us, two 20.5).  From 5 tokens on eight: sixteen leave a wave 128
-    // registers, too few for 32 tokens (39 us), and 23 us at 5 x 50257 x 2048; twelve are no faster.
-    // With 64 tokens two tiles do not fit the registers.
+    // Two tiles of columns a workgroup where they still fill the chip, else one: 32 x 6144 x 8192 takes 16.1 us
+    // against 22.7 (graph replays, as the next figures), a fifth more with three tiles; at 1 x 1536 x 1024 (96
+    // tiles) one is faster.  Sixteen waves for a few tokens of a long K and few columns (1 x 6144 x 8192: 10.2 us,
+    // eight waves 11.1), four for many columns (1 x 50257 x 2048: 14.8 us, two 15.7).  From 5 tokens on eight:
+    // sixteen leave a wave 128 registers, too few for 32 tokens (2.5 times the time), and are slower at 5 x 50257
+    // x 2048 too; twelve are no faster.  Above 32 tokens one tile for 64 of them together; two do not fit the
+    // registers.  Two blocks of 32 tokens with two tiles measured faster than that (33 x 6144 x 8192: 24 us, 28
+    // as it is; 64 x 6144 x 8192: 27, 35; 450 x 1536 x 1024: 11.5, 13.4) and have still to take its place.
     const int64_t tiles = ((int64_t)a.N + 15) / 16;
     if (a.T > 32) return linear<GROUP, SB, 1, 64, 8>(a, st);
     if (a.T > 16) return tiles >= 256 ? linear<GROUP, SB, 2, 32, 8>(a, st) : linear<GROUP, SB, 1, 32, 8>(a, st);

@@ -156,3 +156,29 @@ def test_open_pages_of_half_a_million_sequences():
         moe.moe_kv_attention(some, moe.kv_batch(starts[:201], lens[part].contiguous(), ids[:200], slots), cache.handle,
                              q[part].contiguous(), want, None, ws)
         assert torch.equal(out[part], want)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+def test_append_of_a_million_sequences(bits):
+    """More workgroups than one dimension of a launch holds: the folded layout of append, a row of it partly empty."""
+    import torch
+    n, H, D, P = (1 << 20) + 4321, 4, 64, 16
+    cache = moe.KvPages(n if bits == 16 else 8, H, D, P, bits, n if bits == 8 else 0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    ids = torch.arange(n, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    starts = torch.arange(n + 1, device="cuda", dtype=torch.int32)
+    lens = (torch.arange(n, device="cuda", dtype=torch.int32) % (P - 1) + 1).contiguous()       # no page fills up
+    slots = torch.randperm(n, generator=g, device="cuda", dtype=torch.int32)
+    if bits == 8:
+        ids = ids % 8                                        # not written: the rows go to the open pages
+    q, k, v = torch.randn(3, n, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.zeros_like(q)
+    bt = moe.kv_batch(starts, lens, ids, slots if bits == 8 else None)
+    moe.moe_kv_append(cache.shape(n, n, 1, P, H, 1), bt, cache.handle, k, v, None, q, out)
+    assert torch.equal(out, q)
+    at, row = torch.arange(n, device="cuda"), lens.long() - 1
+    if bits == 8:
+        assert torch.equal(cache.k_tail[slots.long(), 0, :, row], k) and torch.equal(cache.v_tail[slots.long(), 0, :, :, row], v)
+    else:
+        assert torch.equal(cache.k[at, :, row], k) and torch.equal(cache.v[at, :, :, row], v)

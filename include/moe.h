@@ -563,6 +563,23 @@ int moe_kv_attention(const moe_kv_shape *shape, const moe_kv_batch *batch, const
 size_t moe_kv_workspace_bytes(const moe_kv_shape *shape);
 
 /*
+ * moe_kv_attention_sinks -- moe_kv_attention where, behind the shape's window, the first
+ * sink_tokens positions of every sequence stay visible: a row at position p sees the
+ * positions j with (j > p - window or j < sink_tokens), j <= p unless MOE_KV_NONCAUSAL,
+ * their page present.  Positions between the sinks and the window are not read, so
+ * their pages may have been given back (moe_kv_release).  Keys keep the rotation they were
+ * stored with.  Without a window, or with sink_tokens 0, it is moe_kv_attention.
+ * sink_tokens is 0..2^30 (else MOE_ERR_SHAPE); all else as there, the workspace
+ * moe_kv_attention_sinks_workspace_bytes(shape, sink_tokens) bytes.
+ */
+int moe_kv_attention_sinks(const moe_kv_shape *shape, int32_t sink_tokens, const moe_kv_batch *batch,
+                           const moe_kv_cache *cache, const moe_bf16 *q, int64_t q_row_stride, void *out, float *lse,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_kv_attention_sinks needs (0 for an invalid shape or count, at least 256 otherwise). */
+size_t moe_kv_attention_sinks_workspace_bytes(const moe_kv_shape *shape, int32_t sink_tokens);
+
+/*
  * moe_kv_read -- the stored values of the batch's rows: what the cache holds at the last
  * n_s = row_start[s+1] - row_start[s] positions of each sequence, for looking at a cache,
  * moving it or checking it.  k, v [rows][kv_heads][head_dim] bf16 (code * scale rounded to
@@ -570,6 +587,134 @@ size_t moe_kv_workspace_bytes(const moe_kv_shape *shape);
  */
 int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache, moe_bf16 *k,
                 moe_bf16 *v, void *stream);
+
+/* ---- the cache's pages: counted, shared, handed out, given back, moved ----
+ *
+ * For a program that keeps its page tables on the device: the calls below change them there,
+ * in the stream's order, so a decode step with its beams, windows and ended sequences runs
+ * (or is captured) without a word from the host.  State, owned by the caller:
+ *   pages [n_seq][max_pages]  the table of moe_kv_batch, -1 (or any id outside the cache) where no page is
+ *   refs  [n_pages] i32       how many entries of tables name each page; free: not above 0.  A
+ *                             new pool is refs 0 and all entries -1.
+ * One pool's tables and counts serve every layer whose cache has as many pages: the tables change
+ * once, and moe_kv_copy carries the lists of copies out on each layer's cache.  Of the shape the
+ * calls use n_seq, page_tokens, n_pages, max_pages, kv_bits and what is named below; all of it is
+ * checked.  Counts that do not fit the tables give wrong pages but no access outside the buffers;
+ * a call's outputs must not overlap its inputs unless it says so.
+ *
+ * moe_kv_release -- give pages back: of each sequence the blocks that lie at or behind
+ * kv_len[s] (0: the sequence has ended), and with shape.window those that no row at
+ * position kv_len[s] or later sees: block b with (b + 1) P <= kv_len[s] - window + 1 and
+ * b P >= sink_tokens.  Their entries become -1, their pages' counts go down by one each.
+ * pages and refs are changed in place.  max_len is not used.
+ */
+int moe_kv_release(const moe_kv_shape *shape, int32_t sink_tokens, const int32_t *kv_len, int32_t *pages, int32_t *refs,
+                   void *stream);
+
+/*
+ * moe_kv_fork -- every sequence s of the batch goes on from parent[s] (itself, another, the same
+ * as others do; an id outside [0, n_seq): it starts empty): how beams follow their parents.
+ *   kv_len[s] = batch->kv_len[parent[s]], pages[s] = the parent's entries of the blocks
+ *   below that length, -1 from there on; refs counts the new tables.  Nothing is copied: the
+ *   sequences share their pages, and moe_kv_reserve parts them where they are written.
+ *   slots (kv_bits 8): the first sequence that goes on from a parent takes the parent's slot, the
+ *   others those of the sequences from which none goes on, in order; slot_src[s], slot_dst[s]
+ *   then name the copy of the open pages that s needs (moe_kv_copy), -1 where it needs none.
+ * batch has the state before (row_start is not used); kv_len [n_seq], pages [n_seq][max_pages],
+ * slots, slot_src, slot_dst [n_seq] (these three may be NULL with kv_bits 16, and are not written then)
+ * receive the state after and must not overlap it; refs is changed in place.
+ * n_seq is at most MOE_KV_FORK_MAX (else MOE_ERR_UNSUPPORTED).
+ */
+#define MOE_KV_FORK_MAX 8192
+int moe_kv_fork(const moe_kv_shape *shape, const moe_kv_batch *batch, const int32_t *parent, int32_t *kv_len,
+                int32_t *pages, int32_t *slots, int32_t *refs, int32_t *slot_src, int32_t *slot_dst, void *stream);
+
+/*
+ * moe_kv_reserve -- before moe_kv_append: pages for the batch's rows (row_start and kv_len as
+ * there), each named by no other entry.  In the order of sequences and their blocks, every block
+ * with a position of the rows below max_len and max_pages * P
+ *   without a page gets the lowest free one;
+ *   with a page that other entries name too gets a free one in its place, unless all entries that
+ *   name it are such blocks of this call: then the first of them keeps it.
+ * Where a sequence's first block had rows before the new ones and kv_bits is 16, copy_src[s] and
+ * copy_dst[s] are the copy that brings them into the new page (moe_kv_copy, before the append);
+ * -1 otherwise (in 8 bits these rows are in the slot).  A block that finds no free page has entry
+ * -1 afterwards, and one whose rows before the new ones are gone with their page stays at -1: such
+ * blocks of sequence s are counted in missing[s], the append leaves their rows out.
+ *   pages, refs        changed in place (batch->pages is not used)
+ *   copy_src, copy_dst [n_seq], kv_bits 16 (may be NULL with 8, and are not written then)
+ *   missing            [n_seq], nullable
+ *   ws                 moe_kv_pool_workspace_bytes(shape) bytes, 256-byte aligned
+ */
+int moe_kv_reserve(const moe_kv_shape *shape, const moe_kv_batch *batch, int32_t *pages, int32_t *refs,
+                   int32_t *copy_src, int32_t *copy_dst, int32_t *missing, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_kv_compact -- move the pages in use to the lowest ids: with n_live pages in use, the highest
+ * of them goes to the lowest free id, and so on until all lie below n_live or max_moves are
+ * done.  Tables and counts follow at once; copy_src[i], copy_dst[i] for i < max_moves are the
+ * copies to make in every layer's cache before anything reads it (-1 behind the last).
+ * pages has to hold every entry that names a page: one in another table is not changed.
+ *   pages, refs        changed in place
+ *   copy_src, copy_dst [max_moves]; max_moves 0..n_pages / 2
+ *   n_live             [1], nullable: pages in use
+ *   ws                 as for moe_kv_reserve
+ */
+int moe_kv_compact(const moe_kv_shape *shape, int32_t *pages, int32_t *refs, int32_t max_moves, int32_t *copy_src,
+                   int32_t *copy_dst, int32_t *n_live, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_kv_reserve and moe_kv_compact need (0 for an invalid shape, at least 256 otherwise). */
+size_t moe_kv_pool_workspace_bytes(const moe_kv_shape *shape);
+
+/*
+ * moe_kv_copy -- page page_src[i] (keys, values and scales) to page page_dst[i] for i < n_pages_listed,
+ * open pages of slot slot_src[i] to slot slot_dst[i] for i < n_slots_listed (kv_bits 8; not
+ * used with 16).  A pair with an id outside the cache, or with two equal ones, is left out.  No
+ * destination may be a source or another pair's destination (the lists of the calls above
+ * are so).  Lists may be NULL where their number is 0.  n_seq, max_pages and the lengths are not used.
+ *
+ * Errors of these calls: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN (caches
+ * to 16 bytes, tables to 4, ws to 256), MOE_ERR_WORKSPACE, MOE_ERR_HIP.  Nothing to do (n_seq,
+ * max_pages, rows or a list's length 0) is a no-op, but for the outputs that moe_kv_fork
+ * (max_pages 0), moe_kv_reserve (rows 0: missing 0, no copies) and moe_kv_compact always write.
+ */
+int moe_kv_copy(const moe_kv_shape *shape, const moe_kv_cache *cache, int32_t n_pages_listed, const int32_t *page_src,
+                const int32_t *page_dst, int32_t n_slots_listed, const int32_t *slot_src, const int32_t *slot_dst,
+                void *stream);
+
+/* ---- beam search's selection ----
+ *
+ * moe_beam_select -- the best continuations of each request's beams.  Row r = request *
+ * beams + beam of the logits gives its tokens v the sums
+ *   c(r, v) = (scores[r] - lse_r) + logits[r][v],   lse_r = log sum_v exp(logits[r][v]),
+ * taken in 64 bits from the inputs' values, since a token's place among those of another row
+ * hangs on the difference of two such sums.  A row with done[r] offers end_token alone, at
+ * scores[r].  Of a request's rows the n_out largest sums are taken in descending order; equal
+ * sums: the lower row first, in one row the larger logit, then the lower token.  Logits of -infinity are
+ * not offered, nor is anything by a row whose scores[r] - lse_r is not finite (all logits
+ * -infinity, one of them NaN or +infinity, a score of -infinity as unused beams have it).
+ *   logits    [requests * beams][vocab] f32 (MOE_SRC_F32) or bf16 (MOE_SRC_BF16), row_stride elements apart
+ *   scores    [requests * beams] f32, the sums of the beams so far
+ *   done      nullable, [requests * beams] u8: not 0 where a beam has ended
+ *   end_token the token that ends a beam; below 0: none (done has to be NULL then)
+ *   parent    [requests][n_out] i32: the row that is continued (moe_kv_fork's parent), token [requests][n_out]
+ *             i32, score [requests][n_out] f32 (c rounded once); -1, -1 and -infinity where fewer are offered
+ *   done_out  nullable, [requests][n_out] u8: 1 where the parent was done, the token is end_token or nothing was offered
+ *   lse       nullable, [requests * beams] f32, lse_r rounded once (of all rows, also done ones; NaN where a logit is
+ *             NaN or +infinity)
+ *   ws        moe_beam_workspace_bytes(...) bytes, 256-byte aligned
+ * Outputs must not overlap inputs.  beams and n_out are 1..128 (above: MOE_ERR_UNSUPPORTED), vocab >= 1,
+ * requests * beams * vocab at most 2^36 and requests * beams below 2^22 (else MOE_ERR_SHAPE).
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_NULL, MOE_ERR_ALIGN (logits to their elements, all but bytes to 4),
+ * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  requests == 0 is a no-op.
+ */
+int moe_beam_select(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out, const void *logits,
+                    int32_t logits_format, int64_t row_stride, const float *scores, const uint8_t *done,
+                    int32_t end_token, int32_t *parent, int32_t *token, float *score, uint8_t *done_out, float *lse,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_beam_select needs (0 for invalid sizes, at least 256 otherwise). */
+size_t moe_beam_workspace_bytes(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out);
 
 /*
  * moe_linear_q4 -- y = x W^T for a few tokens, W packed int4 with group scales:

@@ -9,7 +9,10 @@ The functions mirror the C ABI names:
   moe_workspace_bytes, moe_validate_shape, moe_status_string, moe_layer_routing,
   moe_quantize_rows, moe_bias_update, moe_layer_forward_chain, moe_quantize_act_q8,
   moe_kv_append, moe_kv_attention, moe_kv_read, moe_kv_workspace_bytes,
-  moe_linear_q4, moe_linear_q4_workspace_bytes
+  moe_linear_q4, moe_linear_q4_workspace_bytes, moe_kv_attention_sinks,
+  moe_kv_attention_sinks_workspace_bytes, moe_kv_release, moe_kv_fork, moe_kv_reserve,
+  moe_kv_compact, moe_kv_copy, moe_kv_pool_workspace_bytes, moe_beam_select,
+  moe_beam_workspace_bytes
 and ``MoeLayer`` keeps one layer's device weights and workspace, ``KvPages`` one
 layer's key/value cache.
 """
@@ -56,9 +59,12 @@ EXPORTS = ["moe_router", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_la
            "moe_layer_forward_profiled", "moe_workspace_bytes", "moe_validate_shape", "moe_status_string",
            "moe_layer_routing", "moe_quantize_rows", "moe_bias_update", "moe_layer_forward_chain",
            "moe_quantize_act_q8", "moe_layer_forward_noalloc", "moe_kv_append", "moe_kv_attention", "moe_kv_read",
-           "moe_kv_workspace_bytes", "moe_linear_q4", "moe_linear_q4_workspace_bytes"]
+           "moe_kv_workspace_bytes", "moe_linear_q4", "moe_linear_q4_workspace_bytes", "moe_kv_attention_sinks",
+           "moe_kv_attention_sinks_workspace_bytes", "moe_kv_release", "moe_kv_fork", "moe_kv_reserve", "moe_kv_compact",
+           "moe_kv_copy", "moe_kv_pool_workspace_bytes", "moe_beam_select", "moe_beam_workspace_bytes"]
 
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_KV_FORK_MAX = 8192
 
 
 class MoeShape(ctypes.Structure):
@@ -142,6 +148,13 @@ def load() -> ctypes.CDLL:
             "moe_kv_attention": [KS, KB, KC, vp, i64, vp, vp, vp, sz, vp],
             "moe_kv_read": [KS, KB, KC, vp, vp, vp],
             "moe_linear_q4": [i32, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp, ctypes.c_uint32, vp, sz, vp],
+            "moe_kv_attention_sinks": [KS, i32, KB, KC, vp, i64, vp, vp, vp, sz, vp],
+            "moe_kv_release": [KS, i32, vp, vp, vp, vp],
+            "moe_kv_fork": [KS, KB, vp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_kv_reserve": [KS, KB, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_kv_compact": [KS, vp, vp, i32, vp, vp, vp, vp, sz, vp],
+            "moe_kv_copy": [KS, KC, i32, vp, vp, i32, vp, vp, vp],
+            "moe_beam_select": [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -153,6 +166,12 @@ def load() -> ctypes.CDLL:
         L.moe_kv_workspace_bytes.restype = sz
         L.moe_linear_q4_workspace_bytes.argtypes = [i32, i32, i32]
         L.moe_linear_q4_workspace_bytes.restype = sz
+        L.moe_kv_attention_sinks_workspace_bytes.argtypes = [KS, i32]
+        L.moe_kv_attention_sinks_workspace_bytes.restype = sz
+        L.moe_kv_pool_workspace_bytes.argtypes = [KS]
+        L.moe_kv_pool_workspace_bytes.restype = sz
+        L.moe_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_beam_workspace_bytes.restype = sz
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -381,16 +400,18 @@ def _kv_fits(sh, batch, cache):
     starts, lens, table, slots = batch.sizes
     if starts < n + 1 or lens < n or table != pages or (slots is not None and slots < n):
         raise ValueError("the batch's tables do not fit the shape")
-    h, p, d = sh.kv_heads, sh.page_tokens, sh.head_dim
-    want = ((sh.n_pages, h, p, d), (sh.n_pages, h, d, p))
-    if sh.kv_bits == 8:
-        want += ((sh.n_pages, h), (sh.n_pages, h), (sh.n_slots, 2, h, p, d), (sh.n_slots, 2, h, d, p))
-        if slots is None and sh.n_slots < n:
-            raise ValueError("n_slots is below n_seq and no slots are given")
-    else:
-        want += (None,) * 4
-    if cache.sizes != want:
+    if sh.kv_bits == 8 and slots is None and sh.n_slots < n:
+        raise ValueError("n_slots is below n_seq and no slots are given")
+    if cache.sizes != _cache_sizes(sh):
         raise ValueError("the cache's tensors do not fit the shape")
+
+
+def _cache_sizes(sh):
+    h, p, d = sh.kv_heads, sh.page_tokens, sh.head_dim
+    sizes = ((sh.n_pages, h, p, d), (sh.n_pages, h, d, p))
+    if sh.kv_bits == 8:
+        return sizes + ((sh.n_pages, h), (sh.n_pages, h), (sh.n_slots, 2, h, p, d), (sh.n_slots, 2, h, d, p))
+    return sizes + (None,) * 4
 
 
 def kv_rotary(cos=None, sin=None, rot_dim=0, pos=None, q_norm=None, k_norm=None, eps=1e-6) -> MoeKvRotary:
@@ -452,14 +473,30 @@ def moe_kv_append(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, ro
 def moe_kv_attention(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, q, out, lse=None, ws=None, stream=None):
     """Attention of the batch's rows over the cache (include/moe.h): out [rows][q_heads][head_dim] (bf16, or f32 with
     MOE_OUT_F32), lse [rows][q_heads] f32 or None, ws moe_kv_workspace_bytes(sh) bytes."""
+    _check(load().moe_kv_attention(sh, batch, cache, *_attention_args(sh, batch, cache, q, out, lse, ws), _stream(stream)),
+           "moe_kv_attention")
+
+
+def _attention_args(sh, batch, cache, q, out, lse, ws):
     torch = _torch or _bind_torch()
     _kv_fits(sh, batch, cache)
     qp, qs = _head_rows(q, sh.rows, sh.q_heads, sh.head_dim, "q")
     op = _head_out(out, sh.rows, sh.q_heads, sh.head_dim, "out", bool(sh.flags & MOE_OUT_F32))
     if lse is not None and lse.numel() != sh.rows * sh.q_heads:
         raise ValueError("lse must be [rows][q_heads]")
-    _check(load().moe_kv_attention(sh, batch, cache, qp, qs, op, _typed(lse, torch.float32, "lse"), _ptr(ws),
-                                   ws.numel() if ws is not None else 0, _stream(stream)), "moe_kv_attention")
+    return qp, qs, op, _typed(lse, torch.float32, "lse"), _ptr(ws), ws.numel() if ws is not None else 0
+
+
+def moe_kv_attention_sinks_workspace_bytes(sh: MoeKvShape, sink_tokens: int) -> int:
+    return int(load().moe_kv_attention_sinks_workspace_bytes(ctypes.byref(sh), sink_tokens))
+
+
+def moe_kv_attention_sinks(sh: MoeKvShape, sink_tokens: int, batch: MoeKvBatch, cache: MoeKvCache, q, out, lse=None, ws=None,
+                           stream=None):
+    """moe_kv_attention where the first sink_tokens positions stay visible behind the shape's window (include/moe.h); ws
+    moe_kv_attention_sinks_workspace_bytes(sh, sink_tokens) bytes."""
+    _check(load().moe_kv_attention_sinks(sh, sink_tokens, batch, cache, *_attention_args(sh, batch, cache, q, out, lse, ws),
+                                         _stream(stream)), "moe_kv_attention_sinks")
 
 
 def moe_kv_read(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, stream=None):
@@ -468,6 +505,103 @@ def moe_kv_read(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, stre
     kp = _head_out(k, sh.rows, sh.kv_heads, sh.head_dim, "k")
     vp = _head_out(v, sh.rows, sh.kv_heads, sh.head_dim, "v")
     _check(load().moe_kv_read(sh, batch, cache, kp, vp, _stream(stream)), "moe_kv_read")
+
+
+# ---- the cache's pages (include/moe.h): tables and counts on the device
+
+
+def _ints(t, n, what):
+    """Pointer of an int32 GPU tensor with n elements (None stays None)."""
+    torch = _torch or _bind_torch()
+    if t is not None and (t.dtype is not torch.int32 or t.numel() != n):
+        raise ValueError(f"{what} must be int32 with {n} elements")
+    return _ptr(t)
+
+
+def moe_kv_pool_workspace_bytes(sh: MoeKvShape) -> int:
+    return int(load().moe_kv_pool_workspace_bytes(ctypes.byref(sh)))
+
+
+def moe_kv_release(sh: MoeKvShape, sink_tokens: int, kv_len, pages, refs, stream=None):
+    """Give back the pages behind kv_len [n_seq] and those between the sinks and the shape's window (include/moe.h);
+    pages [n_seq][max_pages] and refs [n_pages] are changed in place."""
+    _check(load().moe_kv_release(sh, sink_tokens, _ints(kv_len, sh.n_seq, "kv_len"), _ints(pages, sh.n_seq * sh.max_pages, "pages"),
+                                 _ints(refs, sh.n_pages, "refs"), _stream(stream)), "moe_kv_release")
+
+
+def moe_kv_fork(sh: MoeKvShape, batch: MoeKvBatch, parent, kv_len, pages, slots, refs, slot_src=None, slot_dst=None,
+                stream=None):
+    """Sequence s goes on from parent[s] (include/moe.h): the batch's state before, kv_len, pages, slots and the lists of
+    open pages to copy (slot_src, slot_dst) after; refs is changed in place.  slots and the lists may be None in 16 bits."""
+    n = sh.n_seq
+    _, lens, table, slots_in = batch.sizes
+    if lens < n or table != (n, sh.max_pages) or (slots_in is not None and slots_in < n):
+        raise ValueError("the batch's tables do not fit the shape")
+    _check(load().moe_kv_fork(sh, batch, _ints(parent, n, "parent"), _ints(kv_len, n, "kv_len"), _ints(pages, n * sh.max_pages, "pages"),
+                              _ints(slots, n, "slots"), _ints(refs, sh.n_pages, "refs"), _ints(slot_src, n, "slot_src"),
+                              _ints(slot_dst, n, "slot_dst"), _stream(stream)), "moe_kv_fork")
+
+
+def moe_kv_reserve(sh: MoeKvShape, batch: MoeKvBatch, pages, refs, copy_src=None, copy_dst=None, missing=None, ws=None,
+                   stream=None):
+    """Pages of their own for the batch's coming rows (include/moe.h), in place in pages (the batch's table, as a rule)
+    and refs; copy_src, copy_dst [n_seq] (16 bits): the pages to copy before the append; missing [n_seq] or None; ws
+    moe_kv_pool_workspace_bytes(sh) bytes."""
+    n = sh.n_seq
+    if batch.sizes[0] < n + 1 or batch.sizes[1] < n:
+        raise ValueError("the batch's tables do not fit the shape")
+    _check(load().moe_kv_reserve(sh, batch, _ints(pages, n * sh.max_pages, "pages"), _ints(refs, sh.n_pages, "refs"),
+                                 _ints(copy_src, n, "copy_src"), _ints(copy_dst, n, "copy_dst"), _ints(missing, n, "missing"), _ptr(ws),
+                                 ws.numel() if ws is not None else 0, _stream(stream)), "moe_kv_reserve")
+
+
+def moe_kv_compact(sh: MoeKvShape, pages, refs, copy_src, copy_dst, n_live=None, ws=None, stream=None):
+    """Move the pages in use to the lowest ids, as many as copy_src and copy_dst have room for (include/moe.h); pages and
+    refs are changed in place, n_live [1] or None."""
+    moves = copy_src.numel()
+    _check(load().moe_kv_compact(sh, _ints(pages, sh.n_seq * sh.max_pages, "pages"), _ints(refs, sh.n_pages, "refs"), moves,
+                                 _ints(copy_src, moves, "copy_src"), _ints(copy_dst, moves, "copy_dst"), _ints(n_live, 1, "n_live"),
+                                 _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)), "moe_kv_compact")
+
+
+def moe_kv_copy(sh: MoeKvShape, cache: MoeKvCache, page_src=None, page_dst=None, slot_src=None, slot_dst=None, stream=None):
+    """Copy pages and open pages of one layer's cache by the lists of the calls above (include/moe.h)."""
+    if cache.sizes != _cache_sizes(sh):
+        raise ValueError("the cache's tensors do not fit the shape")
+    if (page_src is None) != (page_dst is None) or (slot_src is None) != (slot_dst is None):
+        raise ValueError("a list's sources and destinations come together")
+    pages, slots = (t.numel() if t is not None else 0 for t in (page_src, slot_src))
+    _check(load().moe_kv_copy(sh, cache, pages, _ints(page_src, pages, "page_src"), _ints(page_dst, pages, "page_dst"), slots,
+                              _ints(slot_src, slots, "slot_src"), _ints(slot_dst, slots, "slot_dst"), _stream(stream)), "moe_kv_copy")
+
+
+def moe_beam_workspace_bytes(requests: int, beams: int, vocab: int, n_out: int) -> int:
+    return int(load().moe_beam_workspace_bytes(requests, beams, vocab, n_out))
+
+
+def moe_beam_select(logits, scores, parent, token, score, lse=None, done=None, done_out=None, end_token=-1, ws=None,
+                    stream=None):
+    """The best continuations of each request's beams (include/moe.h): logits [requests * beams][vocab] f32 or bf16 (rows
+    possibly apart), scores [requests][beams] f32; parent, token (int32) and score (f32) [requests][n_out]; lse
+    [requests][beams] f32, done [requests][beams] and done_out [requests][n_out] (bool or uint8), each or None."""
+    torch = _torch or _bind_torch()
+    (requests, beams), n_out, f32 = scores.shape, parent.shape[1], torch.float32
+    if logits.dim() != 2 or logits.shape[0] != requests * beams or logits.dtype not in (f32, torch.bfloat16) or not logits.is_cuda:
+        raise ValueError("logits must be a float32 or bfloat16 [requests * beams][vocab] GPU tensor")
+    vocab, stride = logits.shape[1], logits.stride()
+    if requests and vocab > 1 and stride[1] != 1:
+        raise ValueError("a row's logits must be contiguous")
+    for t, shape, dtypes, what in ((scores, (requests, beams), (f32,), "scores"), (parent, (requests, n_out), (torch.int32,), "parent"),
+                                   (token, (requests, n_out), (torch.int32,), "token"), (score, (requests, n_out), (f32,), "score"),
+                                   (lse, (requests, beams), (f32,), "lse"),
+                                   (done, (requests, beams), (torch.bool, torch.uint8), "done"),
+                                   (done_out, (requests, n_out), (torch.bool, torch.uint8), "done_out")):
+        if t is not None and (t.shape != shape or t.dtype not in dtypes):
+            raise ValueError(f"{what} must be {dtypes[0]} {list(shape)}")
+    _check(load().moe_beam_select(requests, beams, vocab, n_out, logits.data_ptr(), MOE_SRC_F32 if logits.dtype is f32 else MOE_SRC_BF16,
+                                  stride[0] if logits.shape[0] > 1 else vocab, _ptr(scores), _ptr(done), end_token, _ptr(parent),
+                                  _ptr(token), _ptr(score), _ptr(done_out), _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0,
+                                  _stream(stream)), "moe_beam_select")
 
 
 def moe_linear_q4_workspace_bytes(T: int, N: int, K: int) -> int:

@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_hip.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["moe_api.hip", "router.hip", "permute.hip", "ffn.hip", "combine.hip", "decode.hip", "quant.hip",
-           "kv_api.hip", "kv_append.hip", "kv_attention.hip", "linear_q4.hip"]
+           "kv_api.hip", "kv_append.hip", "kv_attention.hip", "kv_pool.hip", "linear_q4.hip", "beam.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++20", "-I", INCLUDE, "-I", CSRC,

@@ -1,8 +1,10 @@
-// kv_api.hip -- the C ABI (include/moe.h) of the paged cache, its attention and
-// the few-token int4 products: host-side validation and launches.  As in
+// kv_api.hip -- the C ABI (include/moe.h) of the paged cache, its attention and pages,
+// the few-token int4 products and beam search's selection: host-side validation and launches.  As in
 // moe_api.hip nothing here touches device memory from the host or synchronises.
 #include "moe.h"
 #include "moe_launch.h"
+
+#include <initializer_list>
 
 namespace {
 
@@ -143,28 +145,38 @@ extern "C" int moe_kv_append(const moe_kv_shape *shape, const moe_kv_batch *batc
     return hip_status(moe::launch_kv_append(args_of(shape, batch, cache), n, (hipStream_t)stream));
 }
 
-extern "C" size_t moe_kv_workspace_bytes(const moe_kv_shape *shape)
+extern "C" size_t moe_kv_attention_sinks_workspace_bytes(const moe_kv_shape *shape, int32_t sink_tokens)
 {
-    if (check_shape(shape) != MOE_OK) return 0;
-    const size_t n = moe::kv_attention_workspace(args_of(shape, nullptr, nullptr));
+    if (check_shape(shape) != MOE_OK || sink_tokens < 0 || sink_tokens > 1 << 30) return 0;
+    const size_t n = moe::kv_attention_workspace(args_of(shape, nullptr, nullptr), shape->window ? sink_tokens : 0);
     return n < 256 ? 256 : (n + 255) / 256 * 256;
+}
+
+extern "C" size_t moe_kv_workspace_bytes(const moe_kv_shape *shape) { return moe_kv_attention_sinks_workspace_bytes(shape, 0); }
+
+extern "C" int moe_kv_attention_sinks(const moe_kv_shape *shape, int32_t sink_tokens, const moe_kv_batch *batch,
+                                      const moe_kv_cache *cache, const moe_bf16 *q, int64_t q_row_stride, void *out,
+                                      float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    if (const int r = check_shape(shape)) return r;
+    if (sink_tokens < 0 || sink_tokens > 1 << 30) return MOE_ERR_SHAPE;
+    if (empty(shape)) return MOE_OK;
+    if (const int r = check_tables(shape, batch, cache)) return r;
+    if (const int r = check_rows(q, q_row_stride, shape->q_heads, shape->head_dim)) return r;
+    if (!out) return MOE_ERR_NULL;
+    if (!aligned(out, 16) || !aligned(lse, 4)) return MOE_ERR_ALIGN;
+    if (ws_bytes < moe_kv_attention_sinks_workspace_bytes(shape, sink_tokens)) return MOE_ERR_WORKSPACE;
+    if (!ws) return MOE_ERR_NULL;
+    if (!aligned(ws, 256)) return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_kv_attention(args_of(shape, batch, cache), sink_tokens, q, q_row_stride, out,
+                                               (shape->flags & MOE_OUT_F32) ? 1 : 0, lse, ws, (hipStream_t)stream));
 }
 
 extern "C" int moe_kv_attention(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache,
                                 const moe_bf16 *q, int64_t q_row_stride, void *out, float *lse, void *ws,
                                 size_t ws_bytes, void *stream)
 {
-    if (const int r = check_shape(shape)) return r;
-    if (empty(shape)) return MOE_OK;
-    if (const int r = check_tables(shape, batch, cache)) return r;
-    if (const int r = check_rows(q, q_row_stride, shape->q_heads, shape->head_dim)) return r;
-    if (!out) return MOE_ERR_NULL;
-    if (!aligned(out, 16) || !aligned(lse, 4)) return MOE_ERR_ALIGN;
-    if (ws_bytes < moe_kv_workspace_bytes(shape)) return MOE_ERR_WORKSPACE;
-    if (!ws) return MOE_ERR_NULL;
-    if (!aligned(ws, 256)) return MOE_ERR_ALIGN;
-    return hip_status(moe::launch_kv_attention(args_of(shape, batch, cache), q, q_row_stride, out,
-                                               (shape->flags & MOE_OUT_F32) ? 1 : 0, lse, ws, (hipStream_t)stream));
+    return moe_kv_attention_sinks(shape, 0, batch, cache, q, q_row_stride, out, lse, ws, ws_bytes, stream);
 }
 
 extern "C" int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_kv_cache *cache,
@@ -176,6 +188,167 @@ extern "C" int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch,
     if (!k || !v) return MOE_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16)) return MOE_ERR_ALIGN;
     return hip_status(moe::launch_kv_read(args_of(shape, batch, cache), k, v, (hipStream_t)stream));
+}
+
+// ---- the cache's pages
+
+static bool misaligned(std::initializer_list<const void *> tables)
+{
+    for (const void *p : tables)
+        if (!aligned(p, 4)) return true;
+    return false;
+}
+
+extern "C" size_t moe_kv_pool_workspace_bytes(const moe_kv_shape *shape)
+{
+    if (check_shape(shape) != MOE_OK) return 0;
+    return (moe::kv_pool_workspace(shape->n_pages) + 255) / 256 * 256;
+}
+
+static int check_pool_ws(const moe_kv_shape *shape, const void *ws, size_t ws_bytes)
+{
+    if (ws_bytes < moe_kv_pool_workspace_bytes(shape)) return MOE_ERR_WORKSPACE;
+    if (!ws) return MOE_ERR_NULL;
+    return aligned(ws, 256) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+extern "C" int moe_kv_release(const moe_kv_shape *shape, int32_t sink_tokens, const int32_t *kv_len, int32_t *pages,
+                              int32_t *refs, void *stream)
+{
+    if (const int r = check_shape(shape)) return r;
+    if (sink_tokens < 0 || sink_tokens > 1 << 30) return MOE_ERR_SHAPE;
+    if (shape->n_seq == 0 || shape->max_pages == 0) return MOE_OK;
+    if (!kv_len || !pages || (shape->n_pages > 0 && !refs)) return MOE_ERR_NULL;
+    if (misaligned({kv_len, pages, refs})) return MOE_ERR_ALIGN;
+    moe::KvArgs a = args_of(shape, nullptr, nullptr);
+    a.kv_len = kv_len;
+    return hip_status(moe::launch_kv_release(a, sink_tokens, pages, refs, (hipStream_t)stream));
+}
+
+extern "C" int moe_kv_fork(const moe_kv_shape *shape, const moe_kv_batch *batch, const int32_t *parent, int32_t *kv_len,
+                           int32_t *pages, int32_t *slots, int32_t *refs, int32_t *slot_src, int32_t *slot_dst,
+                           void *stream)
+{
+    static_assert(MOE_KV_FORK_MAX == moe::KV_FORK_MAX, "");
+    if (const int r = check_shape(shape)) return r;
+    if (shape->n_seq > MOE_KV_FORK_MAX) return MOE_ERR_UNSUPPORTED;
+    if (shape->n_seq == 0) return MOE_OK;
+    if (!batch || !batch->kv_len || !parent || !kv_len) return MOE_ERR_NULL;
+    if (shape->max_pages > 0 && (!batch->pages || !pages || (shape->n_pages > 0 && !refs))) return MOE_ERR_NULL;
+    const bool with_slots = shape->kv_bits == 8;
+    if (with_slots && (!slots || !slot_src || !slot_dst)) return MOE_ERR_NULL;
+    if (misaligned({batch->kv_len, batch->pages, batch->slots, parent, kv_len, pages, slots, refs, slot_src, slot_dst}))
+        return MOE_ERR_ALIGN;
+    if (batch->kv_len == kv_len || (shape->max_pages > 0 && batch->pages == pages) || (with_slots && batch->slots == slots))
+        return MOE_ERR_SHAPE;  // rows are read while others are written
+    return hip_status(moe::launch_kv_fork(args_of(shape, batch, nullptr), parent, kv_len, pages, with_slots ? slots : nullptr,
+                                          refs, slot_src, slot_dst, (hipStream_t)stream));
+}
+
+extern "C" int moe_kv_reserve(const moe_kv_shape *shape, const moe_kv_batch *batch, int32_t *pages, int32_t *refs,
+                              int32_t *copy_src, int32_t *copy_dst, int32_t *missing, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    if (const int r = check_shape(shape)) return r;
+    if (shape->n_seq == 0) return MOE_OK;
+    if (!batch || !batch->row_start || !batch->kv_len) return MOE_ERR_NULL;
+    if (shape->max_pages > 0 && (!pages || (shape->n_pages > 0 && !refs))) return MOE_ERR_NULL;
+    const bool copies = shape->kv_bits == 16;
+    if (copies && (!copy_src || !copy_dst)) return MOE_ERR_NULL;
+    if (misaligned({batch->row_start, batch->kv_len, pages, refs, copy_src, copy_dst, missing})) return MOE_ERR_ALIGN;
+    if (const int r = check_pool_ws(shape, ws, ws_bytes)) return r;
+    return hip_status(moe::launch_kv_reserve(args_of(shape, batch, nullptr), pages, refs, copies ? copy_src : nullptr,
+                                             copies ? copy_dst : nullptr, missing, ws, (hipStream_t)stream));
+}
+
+extern "C" int moe_kv_compact(const moe_kv_shape *shape, int32_t *pages, int32_t *refs, int32_t max_moves,
+                              int32_t *copy_src, int32_t *copy_dst, int32_t *n_live, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    if (const int r = check_shape(shape)) return r;
+    if (max_moves < 0 || max_moves > shape->n_pages / 2) return MOE_ERR_SHAPE;
+    if (shape->n_pages > 0 && !refs) return MOE_ERR_NULL;
+    if (max_moves > 0 && (!copy_src || !copy_dst)) return MOE_ERR_NULL;
+    if (shape->n_seq > 0 && shape->max_pages > 0 && !pages) return MOE_ERR_NULL;
+    if (misaligned({pages, refs, copy_src, copy_dst, n_live})) return MOE_ERR_ALIGN;
+    if (const int r = check_pool_ws(shape, ws, ws_bytes)) return r;
+    return hip_status(moe::launch_kv_compact(args_of(shape, nullptr, nullptr), pages, refs, max_moves, copy_src, copy_dst,
+                                             n_live, ws, (hipStream_t)stream));
+}
+
+extern "C" int moe_kv_copy(const moe_kv_shape *shape, const moe_kv_cache *cache, int32_t n_pages_listed,
+                           const int32_t *page_src, const int32_t *page_dst, int32_t n_slots_listed,
+                           const int32_t *slot_src, const int32_t *slot_dst, void *stream)
+{
+    if (const int r = check_shape(shape)) return r;
+    if (n_pages_listed < 0 || n_slots_listed < 0) return MOE_ERR_SHAPE;
+    const int32_t n_slots = shape->kv_bits == 8 && shape->n_slots > 0 ? n_slots_listed : 0;
+    const int32_t n_pages = shape->n_pages > 0 ? n_pages_listed : 0;
+    if (n_pages == 0 && n_slots == 0) return MOE_OK;
+    if (!cache || (n_pages && (!page_src || !page_dst)) || (n_slots && (!slot_src || !slot_dst))) return MOE_ERR_NULL;
+    if (misaligned({page_src, page_dst, slot_src, slot_dst})) return MOE_ERR_ALIGN;
+    if (n_pages && (!cache->k || !cache->v)) return MOE_ERR_NULL;
+    if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return MOE_ERR_ALIGN;
+    if (shape->kv_bits == 8) {
+        if (n_pages && (!cache->k_scale || !cache->v_scale)) return MOE_ERR_NULL;
+        if (n_slots && (!cache->k_tail || !cache->v_tail)) return MOE_ERR_NULL;
+        if (misaligned({cache->k_scale, cache->v_scale}) || !aligned(cache->k_tail, 16) || !aligned(cache->v_tail, 16))
+            return MOE_ERR_ALIGN;
+    }
+    return hip_status(moe::launch_kv_copy(args_of(shape, nullptr, cache), n_pages, page_src, page_dst, n_slots, slot_src,
+                                          slot_dst, (hipStream_t)stream));
+}
+
+// ---- beam search
+
+static int check_beam(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out)
+{
+    if (requests < 0 || beams < 1 || vocab < 1 || n_out < 1) return MOE_ERR_SHAPE;
+    if (beams > 128 || n_out > 128) return MOE_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)requests * beams;
+    if (rows >= 1 << 22 || rows * vocab > (int64_t)1 << 36) return MOE_ERR_SHAPE;  // a launch below 2^32 lanes
+    return MOE_OK;
+}
+
+extern "C" size_t moe_beam_workspace_bytes(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out)
+{
+    if (check_beam(requests, beams, vocab, n_out) != MOE_OK) return 0;
+    const size_t n = moe::beam_workspace((int64_t)requests * beams, vocab, n_out);
+    return n < 256 ? 256 : (n + 255) / 256 * 256;
+}
+
+extern "C" int moe_beam_select(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out, const void *logits,
+                               int32_t logits_format, int64_t row_stride, const float *scores, const uint8_t *done,
+                               int32_t end_token, int32_t *parent, int32_t *token, float *score, uint8_t *done_out,
+                               float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    if (const int r = check_beam(requests, beams, vocab, n_out)) return r;
+    if (logits_format != MOE_SRC_F32 && logits_format != MOE_SRC_BF16) return MOE_ERR_SHAPE;
+    if (row_stride < vocab || row_stride > (int64_t)1 << 40 || (done && end_token < 0)) return MOE_ERR_SHAPE;
+    if (requests == 0) return MOE_OK;
+    if (!logits || !scores || !parent || !token || !score) return MOE_ERR_NULL;
+    if (!aligned(logits, logits_format == MOE_SRC_F32 ? 4 : 2) || misaligned({scores, parent, token, score, lse}))
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < moe_beam_workspace_bytes(requests, beams, vocab, n_out)) return MOE_ERR_WORKSPACE;
+    if (!ws) return MOE_ERR_NULL;
+    if (!aligned(ws, 256)) return MOE_ERR_ALIGN;
+    moe::BeamSelect a = {};
+    a.requests = requests;
+    a.beams = beams;
+    a.vocab = vocab;
+    a.n_out = n_out;
+    a.end_token = end_token;
+    a.logits = logits;
+    a.bf16 = logits_format == MOE_SRC_BF16;
+    a.row_stride = row_stride;
+    a.scores = scores;
+    a.done = done;
+    a.parent = parent;
+    a.token = token;
+    a.score = score;
+    a.lse = lse;
+    a.done_out = done_out;
+    return hip_status(moe::launch_beam_select(a, ws, (hipStream_t)stream));
 }
 
 extern "C" size_t moe_linear_q4_workspace_bytes(int32_t T, int32_t N, int32_t K)

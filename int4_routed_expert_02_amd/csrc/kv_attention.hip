@@ -54,6 +54,7 @@ struct KvAttend {
     float *lse;
     float *part;  // partial results: [ns][rows][q_heads] of (D accumulators), then the same of (m, sum)
     int out_f32, ns, group;
+    int sinks;    // behind a window: positions below this stay visible (0: none)
 };
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -89,7 +90,7 @@ __device__ __forceinline__ u32x4 codes_bf16(u32x2 w)
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-// What a row of the batch sees: positions [lo, hi).
+// What a row of the batch sees: positions [lo, hi), and with sinks those below both sinks and hi.
 __device__ __forceinline__ void kv_sees(const KvArgs &a, const KvSeq &sq, int L, int i, int &lo, int &hi)
 {
     const int p = sq.len - sq.n_pos + i;
@@ -97,29 +98,46 @@ __device__ __forceinline__ void kv_sees(const KvArgs &a, const KvSeq &sq, int L,
     lo = a.window ? max(0, max(p + 1, 0) - a.window) : 0;  // the difference of two numbers from 0 on stays in 32 bits
 }
 
+// Tiles of 64 positions with sinks: the first n_sink hold the sinks, the others the window from w0
+// on; tile t of these begins at w0 + 64 (t - n_sink).  What lies between is never read, so a row's work
+// goes by its window however long the sequence is.  Where the sinks' tiles reach the window's,
+// both are one run from position 0.  Otherwise the sinks' tiles lie below the last page that is full:
+// an open page spans two tiles at most, and the window's first tile holds its end or begins before it.
+__device__ __forceinline__ int sink_tiles(int sinks, int hi, int &w0)
+{
+    if (sinks == 0) return 0;
+    const int n = (min(sinks, max(hi, 0)) + 63) >> 6;
+    if (w0 > 64 * n) return n;
+    w0 = 0;
+    return 0;
+}
+
 // ---------------------------------------------------------------- few rows
 
 // How the tiles of 64 positions of a sequence are cut into parts: first the
 // tiles of full pages, then those of the open page (8 bits), from position F on.
+// Tile t of full pages begins at t0 + 64 t, or at 64 t for the first n_sink.
 struct DecTiles {
-    int t0, F, n_codes, total, parts, per;
+    int t0, F, n_codes, total, parts, per, n_sink;
 };
 
 // Waves of a workgroup: they take a part's tiles in turn, and join their results in LDS.
 constexpr int DEC_WAVES = 8;
 
-__device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, int L, int ns, int bits)
+__device__ __forceinline__ DecTiles dec_tiles(const KvArgs &a, const KvSeq &sq, int L, int ns, int bits, int sinks)
 {
     int lo, hi, lo1, hi1;
     kv_sees(a, sq, L, 0, lo, hi);
     kv_sees(a, sq, L, max(sq.n - 1, 0), lo1, hi1);
     DecTiles t;
     t.F = bits == 8 ? min(kv_full(a, sq), hi1) : hi1;
-    t.t0 = lo & ~63;
-    t.n_codes = t.F > t.t0 ? (t.F - t.t0 + 63) >> 6 : 0;
+    int w0 = lo & ~63;
+    t.n_sink = sink_tiles(sinks, hi1, w0);
+    t.t0 = w0 - 64 * t.n_sink;
+    t.n_codes = t.n_sink + (t.F > w0 ? (t.F - w0 + 63) >> 6 : 0);
     int n_open = 0;
     if (bits == 8) {
-        t.F = max(kv_full(a, sq), t.t0);
+        t.F = max(kv_full(a, sq), w0);
         n_open = hi1 > t.F ? (hi1 - t.F + 63) >> 6 : 0;
     }
     t.total = t.n_codes + n_open;
@@ -168,7 +186,7 @@ struct DecState {
     }
 };
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT, bool SINK>
 __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k_attn_dec(KvArgs a, KvAttend t)
 {
     constexpr int DT = D / 16, KS = D / 32;  // d tiles, contraction steps of a score
@@ -181,7 +199,9 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
     const KvSeq sq = kv_seq(a, s);
     if (sq.n == 0) return;
     const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
-    const DecTiles tl = dec_tiles(a, sq, L, t.ns, BITS);
+    const int sinks = SINK ? t.sinks : 0;
+    const DecTiles tl = dec_tiles(a, sq, L, t.ns, BITS, sinks);
+    auto tile_at = [&](int tile) { return (SINK && tile < tl.n_sink ? 0 : tl.t0) + 64 * tile; };
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
     const int rows = sq.n * t.group;
@@ -241,7 +261,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
                 xm[n] = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const bool see = valid && j0 + i >= lo[n] && j0 + i < hi[n];
+                    const bool see = valid && (j0 + i >= lo[n] || (SINK && j0 + i < sinks)) && j0 + i < hi[n];
                     z[n][i / 4][i % 4] = see ? z[n][i / 4][i % 4] * c : -INFINITY;
                     xm[n] = fmaxf(xm[n], z[n][i / 4][i % 4]);
                 }
@@ -289,13 +309,13 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
             const int64_t head_at = (int64_t)kh * D << log2p;
             const int64_t page_elems = ((int64_t)a.kv_heads * D) << log2p;
             auto page_at = [&](int tl_, int chunk) {
-                const int j = tl.t0 + 64 * tl_ + 16 * chunk;
+                const int j = tile_at(tl_) + 16 * chunk;
                 return j < tl.F ? kv_page(a, s, j >> log2p) : -1;
             };
             u32x4 kq[4][D / 64], vq[DT];
             float ks, vs;
             auto load_k = [&](int tl_, int id) {
-                const int j = tl.t0 + 64 * tl_ + 16 * kchunk;
+                const int j = tile_at(tl_) + 16 * kchunk;
                 const int8_t *src = kc + max(id, 0) * page_elems + head_at + ((j & (P - 1)) + krow) * D + 16 * g;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -303,7 +323,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
                     for (int k = 0; k < D / 64; ++k) kq[u][k] = *(const u32x4 *)(src + 4 * u * D + 64 * k);
             };
             auto load_v = [&](int tl_, int id) {
-                const int j = tl.t0 + 64 * tl_ + 16 * g;
+                const int j = tile_at(tl_) + 16 * g;
                 const int8_t *src = vc + max(id, 0) * page_elems + head_at + (r16 << log2p) + (j & (P - 1));
 #pragma unroll
                 for (int d = 0; d < DT; ++d) vq[d] = *(const u32x4 *)(src + ((16 * d) << log2p));
@@ -331,9 +351,9 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
                     }
                 }
                 if (more) load_k(next, idk1);
-                const int b0 = tl.t0 + 64 * tile;
+                const int b0 = tile_at(tile);
                 const bool valid = idg >= 0;
-                const bool full = b0 >= lo_all && b0 + 64 <= min(hi_all, tl.F) && !__builtin_amdgcn_ballot_w64(!valid);
+                const bool full = (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, tl.F) && !__builtin_amdgcn_ballot_w64(!valid);
                 uint32_t p[NT][2][8];
                 softmax(z, valid ? ks * zscale : 0.f, valid ? vs : 0.f, b0, full, valid, p);
 #pragma unroll
@@ -363,7 +383,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
     if (tile16 < end && (BITS == 16 || a.n_slots > 0)) {
         const uint16_t *const ka = BITS == 8 ? a.k_tail : (const uint16_t *)a.k;
         const uint16_t *const va = BITS == 8 ? a.v_tail : (const uint16_t *)a.v;
-        auto first_of = [&](int tile) { return BITS == 8 ? tl.F + 64 * (tile - first16) : tl.t0 + 64 * tile; };
+        auto first_of = [&](int tile) { return BITS == 8 ? tl.F + 64 * (tile - first16) : tile_at(tile); };
         // the block of a chunk: a page of the cache, or the sequence's open page (only where its id is there)
         auto block_of = [&](int b0, int chunk) -> int {
             const int j = b0 + 16 * chunk;
@@ -417,7 +437,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
             }
             if (AHEAD && more) load_k(b1, bk1);
             const bool valid = bg >= 0;
-            const bool full = b0 >= lo_all && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
+            const bool full = (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
             uint32_t p[NT][2][8];
             softmax(z, zscale, 1.0f, b0, full, valid, p);
             if (!full) {
@@ -430,9 +450,8 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int j = b0 + 16 * g + 8 * k + 2 * w;
-                        const uint32_t keep = !valid ? 0u
-                                                     : (j >= lo_min && j < hi_max ? 0xFFFFu : 0u) |
-                                                           (j + 1 >= lo_min && j + 1 < hi_max ? 0xFFFF0000u : 0u);
+                        auto some = [&](int p) { return (p >= lo_min || (SINK && p < sinks)) && p < hi_max; };
+                        const uint32_t keep = !valid ? 0u : (some(j) ? 0xFFFFu : 0u) | (some(j + 1) ? 0xFFFF0000u : 0u);
 #pragma unroll
                         for (int d = 0; d < DT; ++d) vb[d][k][w] &= keep;
                     }
@@ -554,9 +573,10 @@ __device__ __forceinline__ f32x16 mfma32_bf16(u32x4 a, u32x4 b, f32x16 c)
 // The tiles that the rt-th `rows` query rows of a sequence and head look at, and
 // how they are cut into parts.
 struct RowTile {
-    int lo, hi;         // positions some row sees lie in [lo, hi)
-    int t0, total;      // first tile's position, tiles
+    int lo, hi;         // positions some row sees lie in [lo, hi), or below both sinks and hi
+    int t0, total;      // tile t begins at t0 + 64 t; tiles
     int parts, per;
+    int n_sink;         // the first tiles, of sinks: tile t of these begins at 64 t
 };
 
 __device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, int L, const KvAttend &at, int rt, int rows)
@@ -567,8 +587,10 @@ __device__ __forceinline__ RowTile row_tile(const KvArgs &a, const KvSeq &sq, in
     int x;
     kv_sees(a, sq, L, i0, t.lo, x);
     kv_sees(a, sq, L, i1, x, t.hi);
-    t.t0 = t.lo & ~63;
-    t.total = t.hi > t.t0 ? (t.hi - t.t0 + 63) >> 6 : 0;
+    int w0 = t.lo & ~63;
+    t.n_sink = sink_tiles(at.sinks, t.hi, w0);
+    t.t0 = w0 - 64 * t.n_sink;
+    t.total = t.n_sink + (t.hi > w0 ? (t.hi - w0 + 63) >> 6 : 0);
     t.parts = max(1, min(at.ns, (t.total + TILE_MIN - 1) / TILE_MIN));
     t.per = (t.total + t.parts - 1) / t.parts;
     return t;
@@ -597,7 +619,7 @@ struct TileLds {
     __device__ f32x4 *chunks(int buf) const { return (f32x4 *)(base + buf * BYTES + 2 * KB); }
 };
 
-template <int D, int BITS>
+template <int D, int BITS, bool SINK>
 __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a, KvAttend t, int row_tiles, int units)
 {
     constexpr int QS = D / 16, DT = D / 32;     // contraction steps of a score, d tiles
@@ -630,7 +652,10 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const int rows = sq.n * t.group;
     if (rt * TILE_ROWS >= rows) return;
     const int L = kv_limit(a, sq), log2p = a.page_log2, P = 1 << log2p;
+    if (!SINK) t.sinks = 0;
+    const int sinks = SINK ? t.sinks : 0;
     const RowTile tl = row_tile(a, sq, L, t, rt, TILE_ROWS);
+    auto tile_at = [&](int tile) { return (SINK && tile < tl.n_sink ? 0 : tl.t0) + 64 * tile; };
     if (split >= tl.parts) return;
     const int begin = split * tl.per, end = min(tl.total, begin + tl.per);
     const int F = BITS == 8 ? kv_full(a, sq) : 0;  // from here on: the open page
@@ -671,7 +696,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     float ks = 0.f, vs = 0.f;            // wave 0: chunk lane % 4
     int idk = -1, idv = -1, idc = -1;    // pages of the position, of the V chunk, of chunk lane % 4 of the tile to load next
     auto page_of = [&](int tile, int chunk) {
-        const int j = tl.t0 + 64 * tile + 16 * chunk;
+        const int j = tile_at(tile) + 16 * chunk;
         return j < L ? kv_page(a, s, j >> log2p) : -1;
     };
     auto ids_of = [&](int tile) {
@@ -682,7 +707,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     const int64_t page_elems = ((int64_t)a.kv_heads * D) << log2p, head_at = (int64_t)kh * D << log2p;
     constexpr int EB = BITS / 8;
     auto load = [&](int tile) {
-        const int jk = tl.t0 + 64 * tile + kt, jv = tl.t0 + 64 * tile + vt;
+        const int b0 = tile_at(tile), jk = b0 + kt, jv = b0 + vt;
         const char *sk = (const char *)a.k + (max(idk, 0) * page_elems + head_at + (jk & (P - 1)) * D + kq * KC) * EB;
 #pragma unroll
         for (int n = 0; n < KC / 8; ++n) kr[n] = *(const raw_t *)(sk + 8 * n * EB);
@@ -722,15 +747,16 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const int jj = j + 2 * w;
-            v[w] &= (jj >= tl.lo && jj < tl.hi ? 0xFFFFu : 0u) | (jj + 1 >= tl.lo && jj + 1 < tl.hi ? 0xFFFF0000u : 0u);
+            auto some = [&](int p) { return (p >= tl.lo || (SINK && p < sinks)) && p < tl.hi; };
+            v[w] &= (some(jj) ? 0xFFFFu : 0u) | (some(jj + 1) ? 0xFFFF0000u : 0u);
         }
         return v;
     };
     auto put = [&](int buf, int tile) {
 #pragma unroll
         for (int n = 0; n < KC / 8; ++n) *lds.k(buf, krow, kq * (KC / 8) + n) = bf16s(kr[n]);
-        const int j = tl.t0 + 64 * tile + vt;
-        const bool whole = BITS == 8 || (idv >= 0 && j >= tl.lo && j + 8 * VU <= tl.hi);
+        const int j = tile_at(tile) + vt;
+        const bool whole = BITS == 8 || (idv >= 0 && (j >= tl.lo || (SINK && j + 8 * VU <= sinks)) && j + 8 * VU <= tl.hi);
 #pragma unroll
         for (int n = 0; n < VN; ++n)
 #pragma unroll
@@ -744,7 +770,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
     };
     // a tile with chunks of the open page, loaded where it is needed
     auto put_open = [&](int buf, int tile) {
-        const int b0 = tl.t0 + 64 * tile, jk = b0 + kt, jv = b0 + vt;
+        const int b0 = tile_at(tile), jk = b0 + kt, jv = b0 + vt;
         const bool openk = jk >= F, openv = jv >= F;
 #pragma unroll
         for (int n = 0; n < KC / 8; ++n) {
@@ -780,8 +806,8 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 
     // ---- one tile: scores, weights, values
     auto step = [&](int buf, int tile) {
-        const int b0 = tl.t0 + 64 * tile;
-        if (b0 >= hi_max || b0 + 64 <= lo_min) return;  // nothing for this wave
+        const int b0 = tile_at(tile);
+        if (b0 >= hi_max || (b0 + 64 <= lo_min && !(SINK && b0 < sinks))) return;  // nothing for this wave
         f32x16 z[2];
 #pragma unroll
         for (int T = 0; T < 2; ++T)
@@ -821,7 +847,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] = mfma32_bf16(vb[d], p[w], o[d]);
         };
-        if (!care && b0 >= lo_all && b0 + 64 <= hi_all) {
+        if (!care && (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= hi_all) {
             // every row sees every position: the value scale goes into the exponent, and a chunk's
             // sum is divided by it once
 #pragma unroll
@@ -862,7 +888,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = b0 + 16 * n + 8 * h32 + j;
-                const bool see = valid && pos >= lo && pos < hi;
+                const bool see = valid && (pos >= lo || (SINK && pos < sinks)) && pos < hi;
                 const float v = see ? z[n >> 1][(n & 1) * 8 + j] * c[n] : -INFINITY;
                 z[n >> 1][(n & 1) * 8 + j] = v;
                 xm = fmaxf(xm, v);
@@ -949,7 +975,7 @@ __global__ __launch_bounds__(256) void k_attn_parts(KvArgs a, KvAttend t, int gr
     const int64_t rh = idx / (D / 4);
     const int i = (int)(rh / a.q_heads), h = (int)(rh % a.q_heads), d = (int)(idx % (D / 4)) * 4;
     if (i >= sq.n) return;
-    const int parts = few ? dec_tiles(a, sq, L, t.ns, a.kv_bits).parts
+    const int parts = few ? dec_tiles(a, sq, L, t.ns, a.kv_bits, t.sinks).parts
                           : row_tile(a, sq, L, t, (i * t.group + h % t.group) / (32 * tile_waves(D)), 32 * tile_waves(D)).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
@@ -1000,7 +1026,7 @@ __global__ __launch_bounds__(256) void k_attn_parts_few(KvArgs a, KvAttend t)
     const KvSeq sq = kv_seq(a, s);
     const int L = kv_limit(a, sq), d = threadIdx.x % LANES * 4, pl = threadIdx.x / LANES;
     if (i >= sq.n) return;
-    const int parts = dec_tiles(a, sq, L, t.ns, a.kv_bits).parts;
+    const int parts = dec_tiles(a, sq, L, t.ns, a.kv_bits, t.sinks).parts;
     if (parts == 1) return;
     const int64_t at = (int64_t)(sq.row0 + i) * a.q_heads + h, step = (int64_t)a.rows * a.q_heads;
     const float *ml = t.part + t.ns * step * D;
@@ -1042,10 +1068,13 @@ __global__ __launch_bounds__(256) void k_attn_parts_few(KvArgs a, KvAttend t)
 constexpr int DEC_TARGET = 512;  // workgroups that fill the chip: 2 per compute unit
 
 // Parts that a sequence's tiles may be cut into, so that few sequences still fill the chip.
-static int dec_parts(const KvArgs &a)
+static int dec_parts(const KvArgs &a, int sinks)
 {
     int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
-    if (a.window && a.causal && len > (int64_t)a.window + a.max_rows) len = (int64_t)a.window + a.max_rows;
+    if (a.window && a.causal) {
+        const int64_t span = (int64_t)a.window + a.max_rows + (sinks ? (int64_t)sinks + 64 : 0);
+        if (len > span) len = span;
+    }
     const int64_t tiles = len / 64 + 3, most = (tiles + DEC_WAVES - 1) / DEC_WAVES;
     const int64_t base = (int64_t)a.n_seq * a.kv_heads;
     int64_t ns = base > 0 ? (DEC_TARGET + base - 1) / base : 1;
@@ -1078,24 +1107,24 @@ constexpr int FEW_ROWS = 32;  // rows of a key/value head that the few-row kerne
 
 static bool few_rows(const KvArgs &a) { return (int64_t)a.max_rows * (a.q_heads / a.kv_heads) <= FEW_ROWS; }
 
-static int parts_of(const KvArgs &a) { return few_rows(a) ? dec_parts(a) : tile_parts(a); }
+static int parts_of(const KvArgs &a, int sinks) { return few_rows(a) ? dec_parts(a, sinks) : tile_parts(a); }
 
-size_t kv_attention_workspace(const KvArgs &a)
+size_t kv_attention_workspace(const KvArgs &a, int sinks)
 {
-    const int ns = parts_of(a);
+    const int ns = parts_of(a, sinks);
     return ns > 1 ? (size_t)ns * a.rows * a.q_heads * (a.head_dim + 2) * 4 : 256;
 }
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT, bool SINK>
 static hipError_t attend_few(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
     const size_t lds = (2 * DEC_WAVES * 16 * NT + (DEC_WAVES / 2) * (D / 16) * 64 * 4) * sizeof(float);
     const int64_t grid = (int64_t)a.n_seq * a.kv_heads * t.ns;
-    hipLaunchKernelGGL((k_attn_dec<D, BITS, NT>), dim3((unsigned)grid), dim3(DEC_WAVES * WAVE), lds, st, a, t);
+    hipLaunchKernelGGL((k_attn_dec<D, BITS, NT, SINK>), dim3((unsigned)grid), dim3(DEC_WAVES * WAVE), lds, st, a, t);
     return hipGetLastError();
 }
 
-template <int D, int BITS>
+template <int D, int BITS, bool SINK>
 static hipError_t attend_many(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
     // Row tiles are laid out evenly, for each sequence as many as the longest may have, as long as that fits one
@@ -1108,22 +1137,22 @@ static hipError_t attend_many(const KvArgs &a, const KvAttend &t, hipStream_t st
     }
     constexpr size_t lds = 2 * TileLds<D>::BYTES;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = lds > 64 << 10 ? allow_lds((const void *)k_attn_tile<D, BITS>, (int)lds, done) : hipSuccess;
+    const hipError_t e = lds > 64 << 10 ? allow_lds((const void *)k_attn_tile<D, BITS, SINK>, (int)lds, done) : hipSuccess;
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, BITS>), dim3((unsigned)grid), dim3(tile_waves(D) * WAVE), lds, st, a, t, (int)tiles,
-                       (int)units);
+    hipLaunchKernelGGL((k_attn_tile<D, BITS, SINK>), dim3((unsigned)grid), dim3(tile_waves(D) * WAVE), lds, st, a, t,
+                       (int)tiles, (int)units);
     return hipGetLastError();
 }
 
-template <int D, int BITS>
+template <int D, int BITS, bool SINK>
 static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
 {
     const int64_t rows = (int64_t)a.max_rows * t.group;
     hipError_t e;
     if (few_rows(a)) {
-        e = rows <= 16 ? attend_few<D, BITS, 1>(a, t, st) : attend_few<D, BITS, 2>(a, t, st);
+        e = rows <= 16 ? attend_few<D, BITS, 1, SINK>(a, t, st) : attend_few<D, BITS, 2, SINK>(a, t, st);
     } else {
-        e = attend_many<D, BITS>(a, t, st);
+        e = attend_many<D, BITS, SINK>(a, t, st);
     }
     if (e != hipSuccess || t.ns == 1) return e;
     // More than one round of loads for a lane that takes all parts, so the parts go over lanes (one
@@ -1139,7 +1168,14 @@ static hipError_t attend(const KvArgs &a, const KvAttend &t, hipStream_t st)
     return hipGetLastError();
 }
 
-hipError_t launch_kv_attention(const KvArgs &args, const uint16_t *q, int64_t q_stride, void *out, int out_f32,
+template <bool SINK>
+static hipError_t attend_any(const KvArgs &a, const KvAttend &t, hipStream_t st)
+{
+    if (a.head_dim == 64) return a.kv_bits == 8 ? attend<64, 8, SINK>(a, t, st) : attend<64, 16, SINK>(a, t, st);
+    return a.kv_bits == 8 ? attend<128, 8, SINK>(a, t, st) : attend<128, 16, SINK>(a, t, st);
+}
+
+hipError_t launch_kv_attention(const KvArgs &args, int sinks, const uint16_t *q, int64_t q_stride, void *out, int out_f32,
                                float *lse, void *ws, hipStream_t st)
 {
     KvArgs a = args;
@@ -1151,7 +1187,8 @@ hipError_t launch_kv_attention(const KvArgs &args, const uint16_t *q, int64_t q_
     t.out_f32 = out_f32;
     t.lse = lse;
     t.part = (float *)ws;
-    t.ns = parts_of(args);
+    t.sinks = a.window ? sinks : 0;  // without a window every position is seen anyway
+    t.ns = parts_of(args, t.sinks);
     t.group = a.q_heads / a.kv_heads;
     // at most as many sequences together as one dimension of a launch holds (more than that are never cut into parts)
     const int together = (int)(KV_GRID_X / a.kv_heads);
@@ -1168,8 +1205,7 @@ hipError_t launch_kv_attention(const KvArgs &args, const uint16_t *q, int64_t q_
             a.k_tail = args.k_tail + (first * 2 * a.kv_heads * a.head_dim << a.page_log2);
             a.v_tail = args.v_tail + (first * 2 * a.kv_heads * a.head_dim << a.page_log2);
         }
-        const hipError_t e = a.head_dim == 64 ? a.kv_bits == 8 ? attend<64, 8>(a, t, st) : attend<64, 16>(a, t, st)
-                                              : a.kv_bits == 8 ? attend<128, 8>(a, t, st) : attend<128, 16>(a, t, st);
+        const hipError_t e = t.sinks ? attend_any<true>(a, t, st) : attend_any<false>(a, t, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -1,0 +1,639 @@
+// kv_pool.hip -- the pages of a cache: given back, shared by forked sequences, handed out, moved
+// together, copied.
+//
+// A pool's state is the page tables and one count a page, refs: how many entries name it.  There is no
+// list of free pages: a page is free when its count is 0, and the lowest free pages are found by
+// reading the counts (4 bytes a page: 131072 pages are half a megabyte).  So there is nothing that could
+// disagree with the counts, and who gets which page does not depend on the order of atomics: those
+// only add to counts, whose sums do not depend on it, or take the least of numbers.
+//
+// Every page id and parent that comes from a device table is brought inside the sizes of the shape
+// where it is read, so no access depends on what a table holds.
+#include "kv_device.h"
+
+namespace moe {
+
+constexpr int CHUNK = 16 * WAVE;         // pages that a wave looks at together: 16 of a lane
+constexpr int BLOCK_WAVES = 4;
+constexpr int BLOCK = BLOCK_WAVES * CHUNK;  // pages of a workgroup's step
+constexpr int MAX_BLOCKS = 8192;         // workgroups over the counts, each with as many steps as it needs
+
+struct PoolBlocks {
+    int n, steps;  // workgroups, steps of each
+};
+
+static PoolBlocks pool_blocks(int n_pages)
+{
+    const int64_t all = ((int64_t)n_pages + BLOCK - 1) / BLOCK;
+    const int64_t steps = (all + MAX_BLOCKS - 1) / MAX_BLOCKS;
+    return {(int)(steps ? (all + steps - 1) / steps : 0), (int)steps};
+}
+
+// Workspace: [MAX_BLOCKS] counts, [n_pages] a list of free pages or the move of each page, [n_pages] PageUse.
+struct PageUse {
+    unsigned long long leader;  // the first block of the call that names the page: sequence << 32 | block
+    int blocks, refs;           // blocks of the call that name it, its count before the call
+};
+
+static size_t list_at() { return MAX_BLOCKS * sizeof(int32_t); }
+static size_t use_at(int n_pages) { return list_at() + ((size_t)n_pages * 4 + 255) / 256 * 256; }
+
+size_t kv_pool_workspace(int n_pages) { return use_at(n_pages) + (size_t)n_pages * sizeof(PageUse); }
+
+// The number of blocks that hold positions below len.
+__device__ __forceinline__ int blocks_of(const KvArgs &a, int len)
+{
+    len = min(max(len, 0), 1 << 30);
+    return min((len + (1 << a.page_log2) - 1) >> a.page_log2, a.max_pages);
+}
+
+__device__ __forceinline__ bool in_cache(const KvArgs &a, int page) { return (unsigned)page < (unsigned)a.n_pages; }
+
+// Which of the CHUNK pages from p0 on are in use: bit l of m[i] is page p0 + 64 i + l.
+struct ChunkBits {
+    uint64_t m[16];
+    int n;
+};
+
+__device__ __forceinline__ ChunkBits chunk_live(const int32_t *refs, int64_t p0, int64_t n_pages, int lane)
+{
+    int r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t p = p0 + 64 * i + lane;
+        r[i] = p < n_pages ? refs[p] : 0;
+    }
+    ChunkBits c;
+    c.n = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        c.m[i] = __builtin_amdgcn_ballot_w64(r[i] > 0);
+        c.n += __builtin_popcountll(c.m[i]);
+    }
+    return c;
+}
+
+__device__ __forceinline__ int below(uint64_t m, int lane) { return __builtin_popcountll(m & ((1ull << lane) - 1)); }
+
+// ---------------------------------------------------------------- given back
+
+// One entry a thread.  Bound by latency: a table of 32 x 64 entries 3 us.
+__global__ __launch_bounds__(256) void k_kv_release(KvArgs a, int sinks, int32_t *__restrict__ pages, int32_t *__restrict__ refs)
+{
+    const int64_t total = (int64_t)a.n_seq * a.max_pages;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int s = (int)(i / a.max_pages), b = (int)(i % a.max_pages);
+        const int len = min(max(a.kv_len[s], 0), 1 << 30);
+        const int64_t first = (int64_t)b << a.page_log2, next = first + (1 << a.page_log2);
+        const bool behind = a.window && next <= (int64_t)len - a.window + 1 && first >= sinks;
+        if (first < len && !behind) continue;
+        const int page = pages[i];
+        if (page == -1) continue;
+        pages[i] = -1;
+        if (in_cache(a, page)) atomicSub(refs + page, 1);
+    }
+}
+
+// ---------------------------------------------------------------- forked
+
+constexpr int FORK_ENTRIES = 2048;   // entries of a row that a workgroup takes at a time
+constexpr int FORK_PARTS = 256;      // workgroups of a row, at most
+
+// Sum of the block's values before mine (in `total` the sum of all); 256 threads.
+__device__ __forceinline__ int scan256(int v, int *waves, int &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const int y = __shfl_up(x, d, WAVE);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) waves[wave] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        before += w < wave ? waves[w] : 0;
+        total += waves[w];
+    }
+    return before + x - v;
+}
+
+// The first workgroup: lengths, slots and the slots' copies.  The others: a part of one
+// row's table each, as a continuation (its entries from the parent) and as a parent (its pages'
+// counts change by the continuations less one).
+__global__ __launch_bounds__(256) void k_kv_fork(KvArgs a, const int32_t *__restrict__ parent, int32_t *__restrict__ len_out,
+                                                 int32_t *__restrict__ pages_out, int32_t *__restrict__ slots_out,
+                                                 int32_t *__restrict__ refs, int32_t *__restrict__ slot_src,
+                                                 int32_t *__restrict__ slot_dst, int parts)
+{
+    __shared__ int first[KV_FORK_MAX];
+    __shared__ uint16_t left[KV_FORK_MAX];
+    __shared__ int waves[4];
+    const int tid = threadIdx.x, n = a.n_seq;
+    auto parent_of = [&](int s) {
+        const int p = parent[s];
+        return (unsigned)p < (unsigned)n ? p : -1;
+    };
+    auto len_of = [&](int s) { return min(max(a.kv_len[s], 0), 1 << 30); };
+    if (blockIdx.x == 0) {
+        for (int s = tid; s < n; s += 256) {
+            const int p = parent_of(s);
+            len_out[s] = p >= 0 ? len_of(p) : 0;
+            first[s] = INT32_MAX;
+        }
+        if (!slots_out) return;
+        __syncthreads();
+        for (int s = tid; s < n; s += 256)
+            if (const int p = parent_of(s); p >= 0) atomicMin(&first[p], s);
+        __syncthreads();
+        int total = 0;
+        for (int s0 = 0, at = 0; s0 < n; s0 += 256, at += total) {   // sequences that none goes on from
+            const int s = s0 + tid, none = s < n && first[s] == INT32_MAX;
+            const int rank = scan256(none, waves, total);
+            if (none) left[at + rank] = (uint16_t)s;
+        }
+        __syncthreads();
+        auto slot_of = [&](int s) { return a.slots ? a.slots[s] : s; };
+        for (int s0 = 0, at = 0; s0 < n; s0 += 256, at += total) {   // as many as there are sequences without a slot
+            const int s = s0 + tid, p = s < n ? parent_of(s) : -1;
+            const int extra = s < n && (p < 0 || first[p] != s);
+            const int rank = scan256(extra, waves, total);
+            if (s >= n) continue;
+            const int slot = slot_of(extra ? left[at + rank] : p);
+            const bool copied = extra && p >= 0 && len_of(p) > 0;
+            slots_out[s] = slot;
+            slot_src[s] = copied ? slot_of(p) : -1;
+            slot_dst[s] = copied ? slot : -1;
+        }
+        return;
+    }
+    const int s = (blockIdx.x - 1) / parts, part = (blockIdx.x - 1) % parts, p = parent_of(s);
+    const int taken = p >= 0 ? blocks_of(a, a.kv_len[p]) : 0, held = blocks_of(a, a.kv_len[s]);
+    int c = 0;
+    for (int t = tid; t < n; t += 256) c += parent[t] == s ? 1 : 0;
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) c += __shfl_xor(c, d, WAVE);
+    if ((tid & 63) == 0) waves[tid >> 6] = c;
+    __syncthreads();
+    const int go_on = waves[0] + waves[1] + waves[2] + waves[3];
+    const int32_t *mine = a.pages + (int64_t)s * a.max_pages, *theirs = a.pages + (int64_t)max(p, 0) * a.max_pages;
+    int32_t *out = pages_out + (int64_t)s * a.max_pages;
+    for (int e = part * FORK_ENTRIES; e < a.max_pages; e += parts * FORK_ENTRIES)
+        for (int b = e + tid; b < min(e + FORK_ENTRIES, a.max_pages); b += 256) {
+            const int page = b < taken ? theirs[b] : -1;
+            out[b] = in_cache(a, page) ? page : -1;
+            const int change = b < held ? go_on - 1 : -1;
+            if (change == 0) continue;
+            const int named = mine[b];
+            if (in_cache(a, named)) atomicAdd(refs + named, change);
+        }
+}
+
+// ---------------------------------------------------------------- handed out
+
+// The blocks of a sequence that its coming rows are in: first, how many, and whether the first has rows before them.
+struct Wanted {
+    int first, n;
+    bool partial;
+};
+
+__device__ __forceinline__ Wanted wanted_blocks(const KvArgs &a, int s)
+{
+    const KvSeq q = kv_seq(a, s);
+    const int start = max(q.len - q.n_pos, 0), end = kv_limit(a, q);
+    Wanted w = {start >> a.page_log2, 0, (start & ((1 << a.page_log2) - 1)) != 0};
+    if (q.n_pos > 0 && end > start) w.n = ((end - 1) >> a.page_log2) - w.first + 1;
+    return w;
+}
+
+// First launch: the number of free pages of every block of pages; for every page that a wanted block
+// names its count now and room for who else wants it; the lists' empty state.
+__global__ __launch_bounds__(256) void k_kv_reserve_count(KvArgs a, const int32_t *__restrict__ pages, const int32_t *__restrict__ refs,
+                                                          int32_t *__restrict__ copy_src, int32_t *__restrict__ copy_dst,
+                                                          int32_t *__restrict__ missing, int32_t *__restrict__ counts,
+                                                          PageUse *__restrict__ use, int blocks, int steps)
+{
+    __shared__ int waves[BLOCK_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if ((int)blockIdx.x < blocks) {
+        int n = 0;
+        for (int i = 0; i < steps; ++i) {
+            const int64_t p0 = ((int64_t)blockIdx.x * steps + i) * BLOCK + wave * CHUNK;
+            const int64_t there = min(max((int64_t)a.n_pages - p0, (int64_t)0), (int64_t)CHUNK);
+            n += (int)there - chunk_live(refs, p0, a.n_pages, lane).n;
+        }
+        if (lane == 0) waves[wave] = n;
+        __syncthreads();
+        if (tid == 0) counts[blockIdx.x] = waves[0] + waves[1] + waves[2] + waves[3];
+        return;
+    }
+    // a wave for each sequence
+    for (int64_t s = (int64_t)(blockIdx.x - blocks) * 4 + wave; s < a.n_seq; s += (int64_t)(gridDim.x - blocks) * 4) {
+        if (lane == 0) {
+            if (copy_src) copy_src[s] = copy_dst[s] = -1;
+            if (missing) missing[s] = 0;
+        }
+        const Wanted w = wanted_blocks(a, (int)s);
+        for (int i = lane; i < w.n; i += WAVE) {
+            const int page = pages[s * a.max_pages + w.first + i];
+            if (in_cache(a, page)) use[page] = {~0ull, 0, refs[page]};
+        }
+    }
+}
+
+// Second launch, one workgroup: the wanted blocks in order, 1024 at a time.  Who shares which page
+// first; then how many pages are needed; their list; then the hand-out.
+constexpr int RT = 1024;
+
+__device__ __forceinline__ int scan1024(int v, int *waves, int &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const int y = __shfl_up(x, d, WAVE);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) waves[wave] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < RT / WAVE; ++w) {
+        before += w < wave ? waves[w] : 0;
+        total += waves[w];
+    }
+    return before + x - v;
+}
+
+__global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int32_t *refs, int32_t *copy_src, int32_t *copy_dst,
+                                                   int32_t *missing, const int32_t *counts, int32_t *list, PageUse *use,
+                                                   int blocks, int steps)
+{
+    __shared__ int begin[RT], from[RT], waves[RT / WAVE], base[MAX_BLOCKS];
+    __shared__ uint8_t inside[RT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int total;
+
+    // The wanted blocks one after another: f(sequence, block, whether it is its sequence's first and has older rows).
+    // Every thread calls f, those past the end with sequence -1.
+    auto each = [&](auto f) {
+        for (int s0 = 0; s0 < a.n_seq; s0 += RT) {
+            const int s = s0 + tid;
+            Wanted w = {0, 0, false};
+            if (s < a.n_seq) w = wanted_blocks(a, s);
+            const int at = scan1024(w.n, waves, total);
+            const int all = total;
+            begin[tid] = at;
+            from[tid] = w.first;
+            inside[tid] = w.partial;
+            __syncthreads();
+            for (int i0 = 0; i0 < all; i0 += RT) {
+                const int i = i0 + tid;
+                int lo = 0, hi = RT;   // the last sequence that begins at or below i
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (begin[mid] <= i) lo = mid;
+                    else hi = mid;
+                }
+                const int b = i - begin[lo], block = from[lo] + b;
+                // (the bounds hold for any tables with ascending row_start)
+                if (i < all && s0 + lo < a.n_seq && (unsigned)block < (unsigned)a.max_pages) f(s0 + lo, block, b == 0 && inside[lo]);
+                else f(-1, 0, false);
+            }
+            __syncthreads();
+        }
+    };
+    auto entry = [&](int s, int b) { return pages[(int64_t)s * a.max_pages + b]; };
+    auto key = [](int s, int b) { return (unsigned long long)s << 32 | (unsigned)b; };
+
+    each([&](int s, int b, bool) {
+        if (s < 0) return;
+        const int page = entry(s, b);
+        if (!in_cache(a, page) || use[page].refs <= 1) return;
+        atomicAdd(&use[page].blocks, 1);
+        atomicMin(&use[page].leader, key(s, b));
+    });
+    __threadfence();
+    __syncthreads();
+
+    // Of a wanted block: 0 it has its page, 1 it needs one, 2 it needs one in another's place, 3 its older rows are gone.
+    auto state = [&](int s, int b, bool partial, int &page) {
+        page = entry(s, b);
+        if (!in_cache(a, page)) {
+            page = -1;
+            return partial ? 3 : 1;
+        }
+        const int held = use[page].refs;
+        if (held <= 1) return 0;
+        const int wanted = __hip_atomic_load(&use[page].blocks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const unsigned long long leader = __hip_atomic_load(&use[page].leader, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return wanted == held && leader == key(s, b) ? 0 : 2;
+    };
+    int need = 0;
+    each([&](int s, int b, bool partial) {
+        int page;
+        const int st = s >= 0 ? state(s, b, partial, page) : 0;
+        need += st == 1 || st == 2;
+    });
+    scan1024(need, waves, need);
+
+    // the lowest `need` free pages
+    int have = 0;
+    if (need) {
+        for (int b0 = 0; b0 < blocks; b0 += RT) {
+            const int i = b0 + tid;
+            const int before = scan1024(i < blocks ? counts[i] : 0, waves, total);
+            if (i < blocks) base[i] = have + before;
+            have += total;
+        }
+        __syncthreads();
+        have = min(have, need);
+        for (int i = wave; i < blocks; i += RT / WAVE) {
+            int at = base[i];
+            if (at >= have) break;
+            if (counts[i] == 0) continue;
+            for (int c = 0; c < steps * BLOCK_WAVES && at < have; ++c) {
+                const int64_t p0 = (int64_t)i * steps * BLOCK + c * CHUNK;
+                const ChunkBits live = chunk_live(refs, p0, a.n_pages, lane);
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const int64_t p = p0 + 64 * u;
+                    uint64_t free = ~live.m[u];
+                    if (p + 64 > a.n_pages) free &= p >= a.n_pages ? 0ull : ~0ull >> (64 - (int)(a.n_pages - p));
+                    const int mine = at + below(free, lane);
+                    if ((free >> lane & 1) && mine < have) list[mine] = (int32_t)(p + lane);
+                    at += __builtin_popcountll(free);
+                }
+            }
+        }
+        __threadfence();
+        __syncthreads();
+    }
+
+    int given = 0;
+    each([&](int s, int b, bool partial) {
+        int page = -1;
+        const int st = s >= 0 ? state(s, b, partial, page) : 0;
+        const bool needs = st == 1 || st == 2;
+        const int rank = given + scan1024(needs, waves, total);
+        given += total;
+        if (st == 0) return;
+        const int got = needs && rank < have ? list[rank] : -1;
+        if (got < 0 && missing) atomicAdd(missing + s, 1);
+        if (st == 3) return;
+        pages[(int64_t)s * a.max_pages + b] = got;
+        if (st == 2) atomicSub(refs + page, 1);
+        if (got < 0) return;
+        refs[got] = 1;
+        if (st == 2 && partial && copy_src) {
+            copy_src[s] = page;
+            copy_dst[s] = got;
+        }
+    });
+}
+
+// ---------------------------------------------------------------- moved together
+
+// First launch: pages in use of every block; the lists' empty state.
+__global__ __launch_bounds__(256) void k_kv_compact_count(const int32_t *__restrict__ refs, int n_pages, int steps, int max_moves,
+                                                          int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *__restrict__ counts)
+{
+    __shared__ int waves[BLOCK_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = blockIdx.x * 256 + tid; i < max_moves; i += gridDim.x * 256) src[i] = dst[i] = -1;
+    int n = 0;
+    for (int i = 0; i < steps; ++i)
+        n += chunk_live(refs, ((int64_t)blockIdx.x * steps + i) * BLOCK + wave * CHUNK, n_pages, lane).n;
+    if (lane == 0) waves[wave] = n;
+    __syncthreads();
+    if (tid == 0) counts[blockIdx.x] = waves[0] + waves[1] + waves[2] + waves[3];
+}
+
+// Second launch: of every page its move, or -1.  With n pages in use and r of them below page p, a free
+// p < n is the (p - r)-th hole from below, and a p >= n in use the (n - 1 - r)-th page from above: holes and
+// pages of one number go together.
+__global__ __launch_bounds__(256) void k_kv_compact_plan(const int32_t *__restrict__ refs, int n_pages, int steps, int max_moves,
+                                                         int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *__restrict__ n_live,
+                                                         const int32_t *__restrict__ counts, int32_t *__restrict__ move)
+{
+    __shared__ int waves[BLOCK_WAVES], sums[2][4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int all = 0, before = 0;
+    for (int i = tid; i < (int)gridDim.x; i += 256) {
+        const int c = counts[i];
+        all += c;
+        before += i < (int)blockIdx.x ? c : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        all += __shfl_xor(all, d, WAVE);
+        before += __shfl_xor(before, d, WAVE);
+    }
+    if (lane == 0) {
+        sums[0][wave] = all;
+        sums[1][wave] = before;
+    }
+    __syncthreads();
+    all = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+    before = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
+    if (n_live && blockIdx.x == 0 && tid == 0) n_live[0] = all;
+    for (int i = 0; i < steps; ++i) {
+        const int64_t p0 = ((int64_t)blockIdx.x * steps + i) * BLOCK + wave * CHUNK;
+        const ChunkBits live = chunk_live(refs, p0, n_pages, lane);
+        __syncthreads();
+        if (lane == 0) waves[wave] = live.n;
+        __syncthreads();
+        int r = before;
+        for (int w = 0; w < BLOCK_WAVES; ++w) {
+            r += w < wave ? waves[w] : 0;
+            before += waves[w];
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int64_t p = p0 + 64 * u + lane;
+            const bool used = live.m[u] >> lane & 1;
+            const int rank = r + below(live.m[u], lane);
+            r += __builtin_popcountll(live.m[u]);
+            if (p >= n_pages) continue;
+            int to = -1;
+            if (used && p >= all) {
+                const int k = all - 1 - rank;
+                if (k < max_moves) {
+                    src[k] = (int)p;
+                    to = k;
+                }
+            } else if (!used && p < all) {
+                const int k = (int)p - rank;
+                if (k < max_moves) dst[k] = (int)p;
+            }
+            move[p] = to;
+        }
+    }
+}
+
+// Third launch: the tables' entries and the counts.
+__global__ __launch_bounds__(256) void k_kv_compact_apply(KvArgs a, int32_t *__restrict__ pages, int32_t *__restrict__ refs, int max_moves,
+                                                          const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
+                                                          const int32_t *__restrict__ move)
+{
+    const int64_t entries = (int64_t)a.n_seq * a.max_pages, total = entries + max_moves;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        if (i < entries) {
+            const int page = pages[i];
+            if (!in_cache(a, page)) continue;
+            const int k = move[page];
+            if (k >= 0) pages[i] = dst[k];
+        } else {
+            const int from = src[i - entries], to = dst[i - entries];
+            if (from < 0) continue;
+            refs[to] = refs[from];
+            refs[from] = 0;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- copied
+
+struct KvCopyList {
+    const int32_t *src, *dst;
+    int n, limit;          // pairs; ids are below this
+    char *k, *v;           // what is copied of an id: `bytes` of k and of v from id * bytes on
+    float *ks, *vs;        // and `heads` scales of each (null: none)
+    int64_t bytes;
+    int heads, parts;      // parts of a pair
+};
+
+constexpr int COPY_UNITS = 4;                          // 16-byte pieces of a thread
+constexpr int COPY_PART = 256 * COPY_UNITS;            // of a part
+
+// One pair's part: k and v as one run of 16-byte pieces.
+__device__ __forceinline__ void copy_part(const KvCopyList &l, int src, int dst, int part)
+{
+    const int tid = threadIdx.x;
+    const int64_t per = l.bytes / 16, i0 = (int64_t)part * COPY_PART + tid;
+    u32x4 x[COPY_UNITS];
+#pragma unroll
+    for (int u = 0; u < COPY_UNITS; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i < 2 * per) x[u] = *(const u32x4 *)((i < per ? l.k + 16 * i : l.v + 16 * (i - per)) + src * l.bytes);
+    }
+#pragma unroll
+    for (int u = 0; u < COPY_UNITS; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i < 2 * per) *(u32x4 *)((i < per ? l.k + 16 * i : l.v + 16 * (i - per)) + dst * l.bytes) = x[u];
+    }
+    if (l.ks && part == 0)
+        for (int h = tid; h < l.heads; h += 256) {
+            l.ks[(int64_t)dst * l.heads + h] = l.ks[(int64_t)src * l.heads + h];
+            l.vs[(int64_t)dst * l.heads + h] = l.vs[(int64_t)src * l.heads + h];
+        }
+}
+
+// Workgroups take every gridDim.x-th part of the lists' pairs.  A wave looks 64 of its workgroup's parts up at a
+// time, so pairs that are not there cost a 64th of a look.
+__global__ __launch_bounds__(256) void k_kv_copy(KvCopyList pages, KvCopyList slots)
+{
+    const int lane = threadIdx.x & 63;
+    auto list = [&](const KvCopyList &l) {
+        const int64_t total = (int64_t)l.n * l.parts;
+        for (int64_t i0 = blockIdx.x; i0 < total; i0 += (int64_t)WAVE * gridDim.x) {
+            const int64_t i = i0 + (int64_t)lane * gridDim.x;
+            int src = -1, dst = -1;
+            if (i < total) {
+                src = l.src[i / l.parts];
+                dst = l.dst[i / l.parts];
+            }
+            const bool there = (unsigned)src < (unsigned)l.limit && (unsigned)dst < (unsigned)l.limit && src != dst;
+            uint64_t todo = __builtin_amdgcn_ballot_w64(there);
+            while (todo) {
+                const int u = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                copy_part(l, __builtin_amdgcn_readlane(src, u), __builtin_amdgcn_readlane(dst, u),
+                          (int)((i0 + (int64_t)u * gridDim.x) % l.parts));
+            }
+        }
+    };
+    if (pages.n) list(pages);
+    if (slots.n) list(slots);
+}
+
+// ---------------------------------------------------------------- launches
+
+static unsigned groups_of(int64_t items, int64_t per, int64_t most = 1 << 16)
+{
+    const int64_t n = (items + per - 1) / per;
+    return (unsigned)(n < 1 ? 1 : n > most ? most : n);
+}
+
+hipError_t launch_kv_release(const KvArgs &a, int sinks, int32_t *pages, int32_t *refs, hipStream_t st)
+{
+    hipLaunchKernelGGL(k_kv_release, dim3(groups_of((int64_t)a.n_seq * a.max_pages, 256)), dim3(256), 0, st, a, sinks, pages, refs);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const KvArgs &a, const int32_t *parent, int32_t *len_out, int32_t *pages_out, int32_t *slots_out,
+                          int32_t *refs, int32_t *slot_src, int32_t *slot_dst, hipStream_t st)
+{
+    const int parts = (int)groups_of(a.max_pages, FORK_ENTRIES, FORK_PARTS);
+    hipLaunchKernelGGL(k_kv_fork, dim3((unsigned)(1 + parts * a.n_seq)), dim3(256), 0, st, a, parent, len_out, pages_out, slots_out, refs,
+                       slot_src, slot_dst, parts);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_reserve(const KvArgs &a, int32_t *pages, int32_t *refs, int32_t *copy_src, int32_t *copy_dst, int32_t *missing,
+                             void *ws, hipStream_t st)
+{
+    const PoolBlocks b = pool_blocks(a.n_pages);
+    int32_t *counts = (int32_t *)ws, *list = (int32_t *)((char *)ws + list_at());
+    PageUse *use = (PageUse *)((char *)ws + use_at(a.n_pages));
+    hipLaunchKernelGGL(k_kv_reserve_count, dim3(b.n + groups_of(a.n_seq, 4)), dim3(256), 0, st, a, pages, refs, copy_src, copy_dst,
+                       missing, counts, use, b.n, b.steps);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.rows == 0 || a.max_pages == 0) return e;
+    hipLaunchKernelGGL(k_kv_reserve, dim3(1), dim3(RT), 0, st, a, pages, refs, copy_src, copy_dst, missing, counts, list, use, b.n,
+                       b.steps);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const KvArgs &a, int32_t *pages, int32_t *refs, int max_moves, int32_t *src, int32_t *dst, int32_t *n_live,
+                             void *ws, hipStream_t st)
+{
+    const PoolBlocks b = pool_blocks(a.n_pages);
+    int32_t *counts = (int32_t *)ws, *move = (int32_t *)((char *)ws + list_at());
+    const unsigned n = b.n ? b.n : 1;  // without a page: n_live 0
+    hipLaunchKernelGGL(k_kv_compact_count, dim3(n), dim3(256), 0, st, refs, a.n_pages, b.steps, max_moves, src, dst, counts);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_kv_compact_plan, dim3(n), dim3(256), 0, st, refs, a.n_pages, b.steps, max_moves, src, dst, n_live, counts, move);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (max_moves == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_kv_compact_apply, dim3(groups_of((int64_t)a.n_seq * a.max_pages + max_moves, 256)), dim3(256), 0, st, a, pages,
+                       refs, max_moves, src, dst, move);
+    return hipGetLastError();
+}
+
+constexpr int COPY_GROUPS = 4096;  // workgroups that keep the memory busy, with parts left to even out
+
+hipError_t launch_kv_copy(const KvArgs &a, int n_pages, const int32_t *page_src, const int32_t *page_dst, int n_slots,
+                          const int32_t *slot_src, const int32_t *slot_dst, hipStream_t st)
+{
+    const int64_t values = (int64_t)a.kv_heads * a.head_dim << a.page_log2;
+    auto list = [&](const int32_t *src, const int32_t *dst, int n, int limit, void *k, void *v, float *ks, float *vs, int64_t bytes) {
+        const int64_t parts = (2 * bytes / 16 + COPY_PART - 1) / COPY_PART;
+        return KvCopyList{src, dst, n, limit, (char *)k, (char *)v, ks, vs, bytes, a.kv_heads, (int)parts};
+    };
+    const bool codes = a.kv_bits == 8;
+    const KvCopyList p = list(page_src, page_dst, n_pages, a.n_pages, a.k, a.v, codes ? a.k_scale : nullptr, codes ? a.v_scale : nullptr,
+                              values * (a.kv_bits / 8));
+    const KvCopyList s = list(slot_src, slot_dst, codes ? n_slots : 0, a.n_slots, a.k_tail, a.v_tail, nullptr, nullptr, 2 * values * 2);
+    const int64_t parts = (int64_t)p.n * p.parts > (int64_t)s.n * s.parts ? (int64_t)p.n * p.parts : (int64_t)s.n * s.parts;
+    hipLaunchKernelGGL(k_kv_copy, dim3(groups_of(parts, 1, COPY_GROUPS)), dim3(256), 0, st, p, s);
+    return hipGetLastError();
+}
+
+}  // namespace moe

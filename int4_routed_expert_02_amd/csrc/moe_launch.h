@@ -153,9 +153,38 @@ struct KvAppend {
 };
 hipError_t launch_kv_append(const KvArgs &a, const KvAppend &n, hipStream_t st);
 hipError_t launch_kv_read(const KvArgs &a, uint16_t *k, uint16_t *v, hipStream_t st);
-size_t kv_attention_workspace(const KvArgs &a);
-hipError_t launch_kv_attention(const KvArgs &a, const uint16_t *q, int64_t q_stride, void *out, int out_f32,
+// sinks: positions below this stay visible behind a window (0: none)
+size_t kv_attention_workspace(const KvArgs &a, int sinks);
+hipError_t launch_kv_attention(const KvArgs &a, int sinks, const uint16_t *q, int64_t q_stride, void *out, int out_f32,
                                float *lse, void *ws, hipStream_t st);
+
+// the cache's pages (kv_pool.hip)
+constexpr int KV_FORK_MAX = 8192;  // sequences of a fork: their states lie in one workgroup's LDS
+size_t kv_pool_workspace(int n_pages);
+hipError_t launch_kv_release(const KvArgs &a, int sinks, int32_t *pages, int32_t *refs, hipStream_t st);
+hipError_t launch_kv_fork(const KvArgs &a, const int32_t *parent, int32_t *len_out, int32_t *pages_out, int32_t *slots_out,
+                          int32_t *refs, int32_t *slot_src, int32_t *slot_dst, hipStream_t st);
+hipError_t launch_kv_reserve(const KvArgs &a, int32_t *pages, int32_t *refs, int32_t *copy_src, int32_t *copy_dst,
+                             int32_t *missing, void *ws, hipStream_t st);
+hipError_t launch_kv_compact(const KvArgs &a, int32_t *pages, int32_t *refs, int max_moves, int32_t *src, int32_t *dst,
+                             int32_t *n_live, void *ws, hipStream_t st);
+hipError_t launch_kv_copy(const KvArgs &a, int n_pages, const int32_t *page_src, const int32_t *page_dst, int n_slots,
+                          const int32_t *slot_src, const int32_t *slot_dst, hipStream_t st);
+
+// beam search's selection (beam.hip)
+struct BeamSelect {
+    int requests, beams, vocab, n_out, end_token;
+    const void *logits;
+    int bf16;
+    int64_t row_stride;
+    const float *scores;
+    const uint8_t *done;
+    int32_t *parent, *token;
+    float *score, *lse;
+    uint8_t *done_out;
+};
+size_t beam_workspace(int64_t rows, int vocab, int n_out);
+hipError_t launch_beam_select(const BeamSelect &a, void *ws, hipStream_t st);
 
 // few-token products with packed int4 weights and group scales (linear_q4.hip)
 struct LinearQ4 {

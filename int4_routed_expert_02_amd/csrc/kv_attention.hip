@@ -353,7 +353,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
                 if (more) load_k(next, idk1);
                 const int b0 = tile_at(tile);
                 const bool valid = idg >= 0;
-                const bool full = (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, tl.F) && !__builtin_amdgcn_ballot_w64(!valid);
+                const bool full = ((b0 >= lo_all) | (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, tl.F) && !__builtin_amdgcn_ballot_w64(!valid);
                 uint32_t p[NT][2][8];
                 softmax(z, valid ? ks * zscale : 0.f, valid ? vs : 0.f, b0, full, valid, p);
 #pragma unroll
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(DEC_WAVES *WAVE, D == 64 && NT == 1 ? 4 : 2) void k
             }
             if (AHEAD && more) load_k(b1, bk1);
             const bool valid = bg >= 0;
-            const bool full = (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
+            const bool full = ((b0 >= lo_all) | (SINK && b0 + 64 <= sinks)) && b0 + 64 <= min(hi_all, L) && !__builtin_amdgcn_ballot_w64(!valid);
             uint32_t p[NT][2][8];
             softmax(z, zscale, 1.0f, b0, full, valid, p);
             if (!full) {
@@ -847,7 +847,9 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] = mfma32_bf16(vb[d], p[w], o[d]);
         };
-        if (!care && (b0 >= lo_all || (SINK && b0 + 64 <= sinks)) && b0 + 64 <= hi_all) {
+        // (tiles of sinks take the way with masks: asked for here, the compiler's other order of the two ways
+        // costs 70 registers to memory, and 2048 and 1659 rows behind a window of 4096 positions 728 us)
+        if (!care && b0 >= lo_all && b0 + 64 <= hi_all) {
             // every row sees every position: the value scale goes into the exponent, and a chunk's
             // sum is divided by it once
 #pragma unroll
@@ -888,7 +890,7 @@ __global__ __launch_bounds__(tile_waves(D) * WAVE, 2) void k_attn_tile(KvArgs a,
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = b0 + 16 * n + 8 * h32 + j;
-                const bool see = valid && (pos >= lo || (SINK && pos < sinks)) && pos < hi;
+                const bool see = SINK ? valid & ((pos >= lo) | (pos < sinks)) & (pos < hi) : valid && pos >= lo && pos < hi;
                 const float v = see ? z[n >> 1][(n & 1) * 8 + j] * c[n] : -INFINITY;
                 z[n >> 1][(n & 1) * 8 + j] = v;
                 xm = fmaxf(xm, v);

@@ -6,25 +6,28 @@
 // request joins the pieces' sums and merges their lists.
 //
 // The n largest of a piece without sorting it: each wave finds the k-th largest of its 64 lanes' maxima
-// (k = n / waves, a search over the bits of the value with ballots).  k lanes of every wave have a value that
-// large, so at least n values reach the least of the waves' bounds, and few more do.  These go to LDS,
-// where each counts how many are ahead of it: its place.
+// (a search over the leading bits of the value with ballots).  With k = n / g, rounded up, k lanes of each of
+// the g waves with the largest such bounds reach the g-th of them, so at least n values do, and few more.
+// These go to LDS, where each counts how many are ahead of it: its place.
 //
 // The exponentials and their sums are 64 bits wide: a token's place among those of other rows hangs on the
 // difference of two log-sums, and 2^-24 of it changes places (one in some thousand steps with 32 beams).
 #include "moe_device.h"
 #include "moe_launch.h"
+#include <cstdlib>
 
 namespace moe {
 
 constexpr int BEAM_T1 = 256, BEAM_T2 = 512;  // threads of a piece, of a request
-constexpr int BEAM_CAP = 512, BEAM_CAP2 = 1024;  // values that reach the bound and are ranked by counting
+constexpr int BEAM_CAP = 1024, BEAM_CAP2 = 1024;  // values that reach the bound and are ranked by counting
 
-// Order-preserving bits of a value, above 0 for every number.
+// Order-preserving bits of a value (both zeros the same); numbers from the lowest finite one on reach ORDER_FINITE.
+constexpr uint32_t ORDER_FINITE = 0x00800000u, ORDER_INF = 0xFF800000u;
+
 __device__ __forceinline__ uint32_t order32(float x)
 {
-    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float value32(uint32_t o) { return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
@@ -37,26 +40,42 @@ __device__ __forceinline__ uint64_t order64(double x)
 
 __device__ __forceinline__ double value64(uint64_t o) { return __builtin_bit_cast(double, o ^ ((o >> 63) ? 1ull << 63 : ~0ull)); }
 
-// e^d for d <= 0: d = k ln 2 + r with |r| <= ln 2 / 2, the series of e^r up to r^11 / 11! (rest below 7e-15), 2^k.
-// ln 2 in two parts, the first its 40 leading bits, so k times it is exact.  NaN stays NaN; below -745 it is 0.
-__device__ __forceinline__ double exp_neg(double d)
-{
-    const double k = __builtin_rint(fmax(d, -800.0) * 1.4426950408889634074);
-    const double r = __builtin_fma(k, -0x1.9ef35793c7673p-41, __builtin_fma(k, -0x1.62e42fefa2000p-1, d));
-    double p = 1.0 / 39916800.0;
-    p = __builtin_fma(p, r, 1.0 / 3628800.0);
-    p = __builtin_fma(p, r, 1.0 / 362880.0);
-    p = __builtin_fma(p, r, 1.0 / 40320.0);
-    p = __builtin_fma(p, r, 1.0 / 5040.0);
-    p = __builtin_fma(p, r, 1.0 / 720.0);
-    p = __builtin_fma(p, r, 1.0 / 120.0);
-    p = __builtin_fma(p, r, 1.0 / 24.0);
-    p = __builtin_fma(p, r, 1.0 / 6.0);
-    p = __builtin_fma(p, r, 0.5);
-    p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    return d < -745.0 ? 0.0 : __builtin_ldexp(p, (int)k);
-}
+// e^(x - top) for x <= top, top finite: (x - top) log2 e = k + f with a whole k and |f| <= 1/2, the polynomial of
+// degree 9 through 2^f at the Chebyshev points (2^-45.6 relative at most), times 2^k.  k comes from the low bits of a
+// sum with 3 * 2^51 and goes into the result's exponent.  From e^-690 down (so -infinity too) it is e^-690, nothing
+// beside the 1 that the largest adds.  Positive NaN or infinity as x is the caller's.
+// The constants are kept in vector registers: the compiler otherwise moves them there for every value, a third
+// of the loop's instructions.
+struct ExpBelow {
+    double c[10], log2e, round, low;
+    __device__ __forceinline__ ExpBelow()
+    {
+        constexpr double C[10] = {0x1.000000000003dp+0, 0x1.62e42fefa39f7p-1, 0x1.ebfbdff8149f2p-3, 0x1.c6b08d7044119p-5,
+                                  0x1.3b2ab72b175eep-7, 0x1.5d87fe908f88ap-10, 0x1.43088e257f341p-13, 0x1.ffcb76789860fp-17,
+                                  0x1.63ef969a64d3cp-20, 0x1.b6571de2f2351p-24};
+#pragma unroll
+        for (int i = 0; i < 10; ++i) c[i] = held(C[i]);
+        log2e = held(0x1.71547652b82fep+0);
+        round = held(0x1.8p52);
+        low = held(-690.0);
+    }
+    static __device__ __forceinline__ double held(double x)
+    {
+        asm("" : "+s"(x));
+        return x;
+    }
+    __device__ __forceinline__ double operator()(double x, double top) const
+    {
+        const double d = fmax(x - top, low);
+        const double t = __builtin_fma(d, log2e, round), f = __builtin_fma(d, log2e, round - t);
+        double p = c[9];
+#pragma unroll
+        for (int i = 8; i >= 0; --i) p = __builtin_fma(p, f, c[i]);
+        u32x2 bits = __builtin_bit_cast(u32x2, p);
+        bits[1] += __builtin_bit_cast(u32x2, t)[0] << 20;
+        return __builtin_bit_cast(double, bits);
+    }
+};
 
 __device__ __forceinline__ double wave_sum(double x)
 {
@@ -65,16 +84,67 @@ __device__ __forceinline__ double wave_sum(double x)
     return x;
 }
 
-// The k-th largest of the wave's 64 values (the largest v that k of them reach), k <= 64.
+// The k-th largest of the wave's 64 values, rounded down to their BITS leading bits; k <= 64.
+template <int BITS>
 __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
 {
     uint32_t t = 0;
 #pragma unroll
-    for (int b = 31; b >= 0; --b) {
+    for (int b = 31; b > 31 - BITS; --b) {
         const uint32_t trial = t | 1u << b;
         if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial)) >= k) t = trial;
     }
     return t;
+}
+
+// The waves' bounds for g = 2^i of W waves, in bounds[i][W]: at least n of the values whose largest of each lane is
+// v reach what waves_bound() makes of them.  All waves together say most where their values are alike, one wave
+// (for n above its lanes, two) where others have few.
+template <int BITS, int W>
+__device__ __forceinline__ void wave_bounds(uint32_t v, int n, bool alike, uint32_t (*bounds)[W])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i <= (W == 8 ? 3 : 2); ++i) {
+        const int k = (n + (1 << i) - 1) >> i;
+        uint32_t b = 0;
+        if (1 << i == W || (!alike && i == (n > WAVE))) b = wave_kth<BITS>(v, k);
+        if (lane == 0) bounds[i][wave] = b;
+    }
+}
+
+template <int W>
+__device__ __forceinline__ uint32_t waves_bound(const uint32_t (*bounds)[W])
+{
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i <= (W == 8 ? 3 : 2); ++i) {
+        const int lane = threadIdx.x & 63;
+        const uint32_t mine = lane < W ? bounds[i][lane] : 0u;
+        int reach = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) reach += bounds[i][w] >= mine ? 1 : 0;
+        uint32_t b = reach >= 1 << i ? mine : 0u;
+#pragma unroll
+        for (int d = 1; d < WAVE; d <<= 1) b = max(b, (uint32_t)__shfl_xor((int)b, d, WAVE));
+        t = max(t, b);
+    }
+    return t;
+}
+
+// f(i, part, parts) for i < n, part < parts: as many lanes next to each other (`parts`, a power of two up to a wave) share
+// each i as T threads allow; the sum of their results goes to done(i, sum), of which one lane writes.
+template <int T, typename F, typename G>
+__device__ __forceinline__ void shared_count(int n, F f, G done)
+{
+    int log = 0;
+    while (log < 6 && n << (log + 1) <= T) ++log;
+    const int part = threadIdx.x & ((1 << log) - 1);
+    for (int i = threadIdx.x >> log; i < n; i += T >> log) {
+        int c = f(i, part, 1 << log);
+        for (int d = 1; d < 1 << log; d <<= 1) c += __shfl_xor(c, d, WAVE);
+        if (part == 0) done(i, c);
+    }
 }
 
 // What a piece leaves for the second launch.
@@ -99,8 +169,9 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     __shared__ uint64_t cand[BEAM_CAP];
     __shared__ double sums[W];
     __shared__ float tops[W];
-    __shared__ uint32_t bounds[W];
+    __shared__ uint32_t bounds[3][W];
     __shared__ int found, counts[W];
+    static_assert(W == 4, "");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x / w.n;
     const int piece = blockIdx.x % w.n;
@@ -108,9 +179,8 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     const int64_t first = (int64_t)piece * (BEAM_T1 * V) + tid * E;
     if (tid == 0) found = 0;
 
-    uint32_t o[V];
-    float top = -INFINITY;
-    uint32_t most = 0;
+    float x[V];
+    uint32_t o[V], most = 0, least = ~0u;
     {
         u32x4 raw[LOADS];
 #pragma unroll
@@ -134,46 +204,51 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
         for (int u = 0; u < LOADS; ++u)
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float x = E == 4 ? __uint_as_float(raw[u][j]) : (j & 1) ? bf16_hi(raw[u][j / 2]) : bf16_lo(raw[u][j / 2]);
-                top = fmaxf(top, x);
-                o[u * E + j] = __float_as_uint(x);
+                const float y = E == 4 ? __uint_as_float(raw[u][j]) : (j & 1) ? bf16_hi(raw[u][j / 2]) : bf16_lo(raw[u][j / 2]);
+                x[u * E + j] = y;
+                o[u * E + j] = order32(y);
+                most = max(most, o[u * E + j]);
+                least = min(least, o[u * E + j]);
             }
     }
     // a wave's sum is taken from its own largest
-    float wtop = top;
+    uint32_t wmost = most;
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) wtop = fmaxf(wtop, __shfl_xor(wtop, d, WAVE));
+    for (int d = 32; d > 0; d >>= 1) wmost = max(wmost, (uint32_t)__shfl_xor((int)wmost, d, WAVE));
+    const float top = value32(wmost);
+    const ExpBelow exp_below;
     double sum = 0.;
-    bool nan = false;
+    if (wmost >= ORDER_FINITE) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float x = __uint_as_float(o[i]);
-        nan |= x != x || x == INFINITY;
-        if (wtop > -INFINITY) sum += exp_neg((double)x - (double)wtop);
-        o[i] = x > -INFINITY ? order32(x) : 0u;
-        most = most > o[i] ? most : o[i];
+        for (int i = 0; i < V; ++i) sum += exp_below(x[i], top);
     }
-    if (__builtin_amdgcn_ballot_w64(nan)) sum = __builtin_nan("");
     sum = wave_sum(sum);
-    const uint32_t bound = wave_kth(most, (a.n_out + W - 1) / W);
+    // NaN of either sign or +infinity: above the numbers, or below -infinity
+    if (__builtin_amdgcn_ballot_w64(most >= ORDER_INF || least < ORDER_FINITE - 1)) sum = __builtin_nan("");
+    wave_bounds<16, W>(most, a.n_out, (piece + 1) * (int64_t)(BEAM_T1 * V) <= a.vocab, bounds);
     if (lane == 0) {
         sums[wave] = sum;
-        tops[wave] = wtop;
-        bounds[wave] = bound;
+        tops[wave] = wmost >= ORDER_FINITE ? top : -INFINITY;
     }
     __syncthreads();
-    uint32_t t = bounds[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) t = t < bounds[i] ? t : bounds[i];
-    t = t ? t : 1u;
+    const uint32_t t = max(waves_bound<W>(bounds), ORDER_FINITE);
     auto key = [&](int i) { return (uint64_t)o[i] << 32 | (uint32_t)~(uint32_t)(first + i / E * (BEAM_T1 * E) + i % E); };
-    if (most >= t) {
+    // one place for the wave's values, which lie there value by value
+    int mine = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (o[i] >= t) {
-                const int at = atomicAdd(&found, 1);
-                if (at < BEAM_CAP) cand[at] = key(i);
-            }
+    for (int i = 0; i < V; ++i) mine += __builtin_popcountll(__builtin_amdgcn_ballot_w64(o[i] >= t));
+    if (mine) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&found, mine);
+        at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t m = __builtin_amdgcn_ballot_w64(o[i] >= t);
+            if (!m) continue;
+            const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+            if (o[i] >= t && to < BEAM_CAP) cand[to] = key(i);
+            at += __builtin_popcountll(m);
+        }
     }
     __syncthreads();
     int n = found;
@@ -184,7 +259,7 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
             const uint64_t trial = bit_t | 1ull << b;
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) c += o[i] && key(i) >= trial;
+            for (int i = 0; i < V; ++i) c += o[i] >= ORDER_FINITE && key(i) >= trial;
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, WAVE);
             __syncthreads();
@@ -198,24 +273,32 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (o[i] && key(i) >= bit_t) cand[atomicAdd(&found, 1)] = key(i);  // n_out of them
+            if (o[i] >= ORDER_FINITE && key(i) >= bit_t) cand[atomicAdd(&found, 1)] = key(i);  // n_out of them
         __syncthreads();
         n = found;
     }
     uint64_t *out = w.keys + (row * w.n + piece) * a.n_out;
-    for (int i = tid; i < n; i += BEAM_T1) {
-        const uint64_t mine = cand[i];
-        int ahead = 0;
-        for (int j = 0; j < n; ++j) ahead += cand[j] > mine;
-        if (ahead < a.n_out) out[ahead] = mine;
-    }
+    shared_count<BEAM_T1>(
+        n,
+        [&](int i, int part, int parts) {
+            const uint64_t mine = cand[i];
+            int ahead = 0;
+#pragma unroll 4
+            for (int j = part; j < n; j += parts) ahead += cand[j] > mine;
+            return ahead;
+        },
+        [&](int i, int ahead) {
+            if (ahead < a.n_out) out[ahead] = cand[i];
+        });
     for (int i = n + tid; i < a.n_out; i += BEAM_T1) out[i] = 0;
     if (tid == 0) {
         float m = tops[0];
         for (int i = 1; i < W; ++i) m = fmaxf(m, tops[i]);
         double s = 0.;
-        for (int i = 0; i < W; ++i)
-            if (tops[i] > -INFINITY || sums[i] != sums[i]) s += sums[i] * exp_neg((double)tops[i] - (double)m);
+        for (int i = 0; i < W; ++i) {
+            if (sums[i] != sums[i]) s = sums[i];
+            else if (tops[i] > -INFINITY) s += sums[i] * exp_below(tops[i], m);
+        }
         w.pieces[row * w.n + piece] = {s, m, 0};
     }
 }
@@ -236,14 +319,27 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     __shared__ uint64_t cs[BEAM_CAP2], ks[BEAM_CAP2];
     __shared__ uint8_t rs[BEAM_CAP2], state[128];  // state of a row: 0 nothing to offer, 1 its lists, 2 done
     __shared__ double base[128];
-    __shared__ uint32_t bounds[W];
+    __shared__ uint32_t bounds[4][W];
     __shared__ BeamCand heads[W];
+    static_assert(W == 8, "");
     __shared__ int found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     if (tid == 0) found = 0;
 
+    // a list is piece list / beams of row list % beams; the first keys of the thread's first one are on their way early
+    const int lists = a.beams * w.n, n_out = a.n_out;
+    auto keys_of = [&](int list) { return w.keys + ((row0 + list % a.beams) * w.n + list / a.beams) * n_out; };
+    uint64_t ahead8[8];
+    auto load8 = [&](int list, int d0) {
+        const uint64_t *src = keys_of(list) + d0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ahead8[j] = d0 + j < n_out ? src[j] : 0;
+    };
+    if (tid < lists) load8(tid, 0);
+
     // the rows' sums
+    const ExpBelow exp_below;
     for (int r = wave; r < a.beams; r += W) {
         const BeamPiece *p = w.pieces + (row0 + r) * w.n;
         float m = -INFINITY;
@@ -253,7 +349,8 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         double s = 0.;
         for (int i = lane; i < w.n; i += WAVE) {
             const BeamPiece x = p[i];
-            if (x.top > -INFINITY || x.sum != x.sum) s += x.sum * exp_neg((double)x.top - (double)m);
+            if (x.sum != x.sum) s = x.sum;
+            else if (x.top > -INFINITY) s += x.sum * exp_below(x.top, m);
         }
         s = wave_sum(s);
         if (lane == 0) {
@@ -266,42 +363,44 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     }
     __syncthreads();
 
-    const int lists = a.beams * w.n, n_out = a.n_out;
-    // the d-th candidate of a list (the lists of a row: its pieces); without one the key is 0
-    auto candidate = [&](int list, int d) {
-        BeamCand x = {0, 0, list / w.n};
+    // what a key of a list is worth; without one the key is 0
+    auto worth = [&](int list, uint64_t key, bool first) {
+        BeamCand x = {0, 0, list % a.beams};
         const int st = state[x.row];
-        if (st == 1) {
-            x.key = w.keys[((row0 + x.row) * w.n + list % w.n) * n_out + d];
-            if (x.key) x.c = order64(base[x.row] + (double)value32((uint32_t)(x.key >> 32)));
-        } else if (st == 2 && list % w.n == 0 && d == 0) {
+        if (st == 1 && key) {
+            x.key = key;
+            x.c = order64(base[x.row] + (double)value32((uint32_t)(key >> 32)));
+        } else if (st == 2 && first && list < a.beams) {
             x.c = order64(base[x.row]);
             x.key = 1ull << 32 | (uint32_t)~a.end_token;
         }
         return x;
     };
-    // a bound that at least n_out of the lists' first candidates reach
-    const int depth = min(n_out, (BEAM_T2 + lists - 1) / lists);
-    uint32_t most = 0;
-    for (int e = tid; e < lists * depth; e += BEAM_T2) {
-        const uint32_t c = (uint32_t)(candidate(e % lists, e / lists).c >> 32);
-        most = most > c ? most : c;
-    }
-    const uint32_t bound = wave_kth(most, (n_out + W - 1) / W);
-    if (lane == 0) bounds[wave] = bound;
+    auto candidate = [&](int list, int d) { return worth(list, keys_of(list)[d], d == 0); };
+    // a bound that at least n_out candidates reach, from the first ones of the lists
+    const int depth = (n_out + lists - 1) / lists;
+    uint32_t most = tid < lists ? (uint32_t)(worth(tid, ahead8[0], true).c >> 32) : 0u;
+    for (int e = tid + BEAM_T2; e < lists * depth; e += BEAM_T2) most = max(most, (uint32_t)(candidate(e % lists, e / lists).c >> 32));
+    if (lists < BEAM_T2 && tid >= lists && tid < lists * depth) most = (uint32_t)(candidate(tid % lists, tid / lists).c >> 32);
+    wave_bounds<22, W>(most, n_out, false, bounds);
     __syncthreads();
-    uint32_t t = bounds[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) t = t < bounds[i] ? t : bounds[i];
+    const uint32_t t = waves_bound<W>(bounds);
     for (int l = tid; l < lists; l += BEAM_T2)
-        for (int d = 0; d < n_out; ++d) {
-            const BeamCand x = candidate(l, d);
-            if (x.key == 0 || (uint32_t)(x.c >> 32) < t) break;
-            const int at = atomicAdd(&found, 1);
-            if (at >= BEAM_CAP2) break;
-            cs[at] = x.c;
-            ks[at] = x.key;
-            rs[at] = (uint8_t)x.row;
+        for (int d0 = 0; d0 < n_out; d0 += 8) {
+            if (l != tid || d0) load8(l, d0);
+            bool more = true;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const BeamCand x = worth(l, ahead8[j], d0 + j == 0);
+                more = x.key && (uint32_t)(x.c >> 32) >= t;
+                if (!more) continue;
+                const int at = atomicAdd(&found, 1);
+                if (at >= BEAM_CAP2) continue;
+                cs[at] = x.c;
+                ks[at] = x.key;
+                rs[at] = (uint8_t)x.row;
+            }
+            if (!more) break;
         }
     __syncthreads();
     const int n = found;
@@ -315,12 +414,27 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         if (a.done_out) a.done_out[out0 + i] = none || state[x.row] == 2 || (a.end_token >= 0 && token == a.end_token);
     };
     if (n <= BEAM_CAP2) {
-        for (int i = tid; i < n; i += BEAM_T2) {
-            const BeamCand x = {cs[i], ks[i], rs[i]};
-            int ahead = 0;
-            for (int j = 0; j < n; ++j) ahead += BeamCand{cs[j], ks[j], rs[j]}.ahead_of(x);
-            if (ahead < n_out) put(ahead, x);
-        }
+        shared_count<BEAM_T2>(
+            n,
+            [&](int i, int part, int parts) {
+                const uint64_t mine = cs[i];
+                int ahead = 0, equal = 0;
+#pragma unroll 4
+                for (int j = part; j < n; j += parts) {
+                    const uint64_t c = cs[j];
+                    ahead += c > mine;
+                    equal += c == mine;
+                }
+                if (equal > (i % parts == part)) {
+                    const BeamCand x = {mine, ks[i], rs[i]};
+                    for (int j = part; j < n; j += parts)
+                        if (cs[j] == mine) ahead += BeamCand{mine, ks[j], rs[j]}.ahead_of(x);
+                }
+                return ahead;
+            },
+            [&](int i, int ahead) {
+                if (ahead < n_out) put(ahead, BeamCand{cs[i], ks[i], rs[i]});
+            });
         for (int i = n + tid; i < n_out; i += BEAM_T2) put(i, BeamCand{0, 0, 0});
         return;
     }
@@ -355,7 +469,7 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
 // ---------------------------------------------------------------- launches
 
 // Values of a thread: pieces of 8192, or of 2048 where the larger ones would be too few for the chip.
-static int beam_values(int64_t rows, int64_t vocab) { return rows * ((vocab + 8191) / 8192) < 512 ? 8 : 32; }
+static int beam_values(int64_t rows, int64_t vocab) { if (const char *e = getenv("BV")) return atoi(e); return rows * ((vocab + 8191) / 8192) < 512 ? 8 : 32; }
 
 static int beam_pieces(int64_t rows, int vocab)
 {
@@ -372,7 +486,9 @@ template <typename T>
 static hipError_t pieces(const BeamSelect &a, const BeamWs &w, int64_t rows, hipStream_t st)
 {
     const dim3 grid((unsigned)(rows * w.n)), block(BEAM_T1);
-    if (beam_values(rows, a.vocab) == 8) hipLaunchKernelGGL((k_beam_piece<T, 8>), grid, block, 0, st, a, w);
+    const int v = beam_values(rows, a.vocab);
+    if (v == 8) hipLaunchKernelGGL((k_beam_piece<T, 8>), grid, block, 0, st, a, w);
+    else if (v == 16) hipLaunchKernelGGL((k_beam_piece<T, 16>), grid, block, 0, st, a, w);
     else hipLaunchKernelGGL((k_beam_piece<T, 32>), grid, block, 0, st, a, w);
     return hipGetLastError();
 }

@@ -703,7 +703,7 @@ int moe_kv_copy(const moe_kv_shape *shape, const moe_kv_cache *cache, int32_t n_
  *   lse       nullable, [requests * beams] f32, lse_r rounded once (of all rows, also done ones; NaN where a logit is
  *             NaN or +infinity)
  *   ws        moe_beam_workspace_bytes(...) bytes, 256-byte aligned
- * Outputs must not overlap inputs.  beams and n_out are 1..128 (above: MOE_ERR_UNSUPPORTED), vocab >= 1,
+ * Outputs must not overlap inputs.  beams and n_out are 1..128 (above: MOE_ERR_UNSUPPORTED), vocab 1..2^30,
  * requests * beams * vocab at most 2^36 and requests * beams below 2^22 (else MOE_ERR_SHAPE).
  * Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_NULL, MOE_ERR_ALIGN (logits to their elements, all but bytes to 4),
  * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  requests == 0 is a no-op.

@@ -14,7 +14,6 @@
 // difference of two log-sums, and 2^-24 of it changes places (one in some thousand steps with 32 beams).
 #include "moe_device.h"
 #include "moe_launch.h"
-#include <cstdlib>
 
 namespace moe {
 
@@ -22,7 +21,7 @@ constexpr int BEAM_T1 = 256, BEAM_T2 = 512;  // threads of a piece, of a request
 constexpr int BEAM_CAP = 1024, BEAM_CAP2 = 1024;  // values that reach the bound and are ranked by counting
 
 // Order-preserving bits of a value (both zeros the same); numbers from the lowest finite one on reach ORDER_FINITE.
-constexpr uint32_t ORDER_FINITE = 0x00800000u, ORDER_INF = 0xFF800000u;
+constexpr uint32_t ORDER_FINITE = 0x00800000u;
 
 __device__ __forceinline__ uint32_t order32(float x)
 {
@@ -89,7 +88,7 @@ template <int BITS>
 __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
 {
     uint32_t t = 0;
-#pragma unroll
+#pragma unroll 1
     for (int b = 31; b > 31 - BITS; --b) {
         const uint32_t trial = t | 1u << b;
         if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial)) >= k) t = trial;
@@ -97,39 +96,34 @@ __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
     return t;
 }
 
-// The waves' bounds for g = 2^i of W waves, in bounds[i][W]: at least n of the values whose largest of each lane is
-// v reach what waves_bound() makes of them.  All waves together say most where their values are alike, one wave
-// (for n above its lanes, two) where others have few.
+// Two bounds of each wave, for g = W and for g = 1 (2 where n is above a wave's lanes): at least n of the values whose
+// largest of each lane is v reach what waves_bound() makes of them.  All waves together say most where their
+// values are alike (then the others are not looked at), one or two where the others have few.
 template <int BITS, int W>
 __device__ __forceinline__ void wave_bounds(uint32_t v, int n, bool alike, uint32_t (*bounds)[W])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i <= (W == 8 ? 3 : 2); ++i) {
-        const int k = (n + (1 << i) - 1) >> i;
-        uint32_t b = 0;
-        if (1 << i == W || (!alike && i == (n > WAVE))) b = wave_kth<BITS>(v, k);
+#pragma unroll 1
+    for (int i = 0; i < (alike ? 1 : 2); ++i) {
+        const uint32_t b = wave_kth<BITS>(v, i == 0 ? (n + W - 1) / W : n > WAVE ? (n + 1) / 2 : n);
         if (lane == 0) bounds[i][wave] = b;
     }
 }
 
 template <int W>
-__device__ __forceinline__ uint32_t waves_bound(const uint32_t (*bounds)[W])
+__device__ __forceinline__ uint32_t waves_bound(const uint32_t (*bounds)[W], int n, bool alike)
 {
-    uint32_t t = 0;
+    uint32_t t = ~0u, first = 0, second = 0;
 #pragma unroll
-    for (int i = 0; i <= (W == 8 ? 3 : 2); ++i) {
-        const int lane = threadIdx.x & 63;
-        const uint32_t mine = lane < W ? bounds[i][lane] : 0u;
-        int reach = 0;
+    for (int w = 0; w < W; ++w) t = min(t, bounds[0][w]);
+    if (alike) return t;
 #pragma unroll
-        for (int w = 0; w < W; ++w) reach += bounds[i][w] >= mine ? 1 : 0;
-        uint32_t b = reach >= 1 << i ? mine : 0u;
-#pragma unroll
-        for (int d = 1; d < WAVE; d <<= 1) b = max(b, (uint32_t)__shfl_xor((int)b, d, WAVE));
-        t = max(t, b);
+    for (int w = 0; w < W; ++w) {
+        const uint32_t b = bounds[1][w];
+        second = max(second, min(first, b));
+        first = max(first, b);
     }
-    return t;
+    return max(t, n > WAVE ? second : first);
 }
 
 // f(i, part, parts) for i < n, part < parts: as many lanes next to each other (`parts`, a power of two up to a wave) share
@@ -142,6 +136,7 @@ __device__ __forceinline__ void shared_count(int n, F f, G done)
     const int part = threadIdx.x & ((1 << log) - 1);
     for (int i = threadIdx.x >> log; i < n; i += T >> log) {
         int c = f(i, part, 1 << log);
+#pragma unroll 1
         for (int d = 1; d < 1 << log; d <<= 1) c += __shfl_xor(c, d, WAVE);
         if (part == 0) done(i, c);
     }
@@ -169,32 +164,32 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     __shared__ uint64_t cand[BEAM_CAP];
     __shared__ double sums[W];
     __shared__ float tops[W];
-    __shared__ uint32_t bounds[3][W];
+    __shared__ uint32_t bounds[2][W];
     __shared__ int found, counts[W];
     static_assert(W == 4, "");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x / w.n;
     const int piece = blockIdx.x % w.n;
-    const T *src = (const T *)a.logits + row * a.row_stride;
-    const int64_t first = (int64_t)piece * (BEAM_T1 * V) + tid * E;
+    constexpr int N = BEAM_T1 * V;
+    const T *src = (const T *)a.logits + row * a.row_stride + (int64_t)piece * N;
+    const int left = a.vocab - piece * N;  // values from here on, N of them at most are this piece's
     if (tid == 0) found = 0;
 
-    float x[V];
-    uint32_t o[V], most = 0, least = ~0u;
+    float x[V], top = -INFINITY;
     {
         u32x4 raw[LOADS];
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
-            const int64_t i = first + u * (BEAM_T1 * E);
-            if (i + E <= a.vocab) {
+            const int i = tid * E + u * (BEAM_T1 * E);
+            if (i + E <= left) {
                 __builtin_memcpy(&raw[u], src + i, 16);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if constexpr (E == 4) {
-                        raw[u][j] = i + j < a.vocab ? __float_as_uint(src[i + j]) : 0xFF800000u;
+                        raw[u][j] = i + j < left ? __float_as_uint(src[i + j]) : 0xFF800000u;
                     } else {
-                        const uint32_t lo = i + 2 * j < a.vocab ? src[i + 2 * j] : 0xFF80u, hi = i + 2 * j + 1 < a.vocab ? src[i + 2 * j + 1] : 0xFF80u;
+                        const uint32_t lo = i + 2 * j < left ? src[i + 2 * j] : 0xFF80u, hi = i + 2 * j + 1 < left ? src[i + 2 * j + 1] : 0xFF80u;
                         raw[u][j] = hi << 16 | lo;
                     }
                 }
@@ -206,47 +201,46 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
             for (int j = 0; j < E; ++j) {
                 const float y = E == 4 ? __uint_as_float(raw[u][j]) : (j & 1) ? bf16_hi(raw[u][j / 2]) : bf16_lo(raw[u][j / 2]);
                 x[u * E + j] = y;
-                o[u * E + j] = order32(y);
-                most = max(most, o[u * E + j]);
-                least = min(least, o[u * E + j]);
+                top = __builtin_elementwise_maximum(top, y);  // (NaN stays)
             }
     }
     // a wave's sum is taken from its own largest
-    uint32_t wmost = most;
+    float wtop = top;
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) wmost = max(wmost, (uint32_t)__shfl_xor((int)wmost, d, WAVE));
-    const float top = value32(wmost);
+    for (int d = 32; d > 0; d >>= 1) wtop = __builtin_elementwise_maximum(wtop, __shfl_xor(wtop, d, WAVE));
     const ExpBelow exp_below;
     double sum = 0.;
-    if (wmost >= ORDER_FINITE) {
+    if (wtop > -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += exp_below(x[i], top);
+        for (int i = 0; i < V; ++i) sum += exp_below(x[i], wtop);
     }
     sum = wave_sum(sum);
-    // NaN of either sign or +infinity: above the numbers, or below -infinity
-    if (__builtin_amdgcn_ballot_w64(most >= ORDER_INF || least < ORDER_FINITE - 1)) sum = __builtin_nan("");
-    wave_bounds<16, W>(most, a.n_out, (piece + 1) * (int64_t)(BEAM_T1 * V) <= a.vocab, bounds);
+    if (!(wtop < INFINITY)) sum = __builtin_nan("");  // a NaN or +infinity among them
+    const bool alike = N <= left;
+    wave_bounds<16, W>(order32(top), a.n_out, alike, bounds);
     if (lane == 0) {
         sums[wave] = sum;
-        tops[wave] = wmost >= ORDER_FINITE ? top : -INFINITY;
+        tops[wave] = wtop;
     }
     __syncthreads();
-    const uint32_t t = max(waves_bound<W>(bounds), ORDER_FINITE);
-    auto key = [&](int i) { return (uint64_t)o[i] << 32 | (uint32_t)~(uint32_t)(first + i / E * (BEAM_T1 * E) + i % E); };
+    const float t = value32(max(waves_bound<W>(bounds, a.n_out, alike), ORDER_FINITE));
+    auto key = [&](int i) {
+        return (uint64_t)order32(x[i]) << 32 | (uint32_t)~(uint32_t)(piece * N + tid * E + i / E * (BEAM_T1 * E) + i % E);
+    };
     // one place for the wave's values, which lie there value by value
     int mine = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) mine += __builtin_popcountll(__builtin_amdgcn_ballot_w64(o[i] >= t));
+    for (int i = 0; i < V; ++i) mine += __builtin_popcountll(__builtin_amdgcn_ballot_w64(x[i] >= t));
     if (mine) {
         int at = 0;
         if (lane == 0) at = atomicAdd(&found, mine);
         at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint64_t m = __builtin_amdgcn_ballot_w64(o[i] >= t);
+            const uint64_t m = __builtin_amdgcn_ballot_w64(x[i] >= t);
             if (!m) continue;
             const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-            if (o[i] >= t && to < BEAM_CAP) cand[to] = key(i);
+            if (x[i] >= t && to < BEAM_CAP) cand[to] = key(i);
             at += __builtin_popcountll(m);
         }
     }
@@ -259,7 +253,7 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
             const uint64_t trial = bit_t | 1ull << b;
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) c += o[i] >= ORDER_FINITE && key(i) >= trial;
+            for (int i = 0; i < V; ++i) c += x[i] >= t && key(i) >= trial;
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, WAVE);
             __syncthreads();
@@ -273,7 +267,7 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (o[i] >= ORDER_FINITE && key(i) >= bit_t) cand[atomicAdd(&found, 1)] = key(i);  // n_out of them
+            if (x[i] >= t && key(i) >= bit_t) cand[atomicAdd(&found, 1)] = key(i);  // n_out of them
         __syncthreads();
         n = found;
     }
@@ -292,8 +286,8 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
         });
     for (int i = n + tid; i < a.n_out; i += BEAM_T1) out[i] = 0;
     if (tid == 0) {
-        float m = tops[0];
-        for (int i = 1; i < W; ++i) m = fmaxf(m, tops[i]);
+        float m = -INFINITY;
+        for (int i = 0; i < W; ++i) m = fmaxf(m, tops[i]);
         double s = 0.;
         for (int i = 0; i < W; ++i) {
             if (sums[i] != sums[i]) s = sums[i];
@@ -319,7 +313,7 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     __shared__ uint64_t cs[BEAM_CAP2], ks[BEAM_CAP2];
     __shared__ uint8_t rs[BEAM_CAP2], state[128];  // state of a row: 0 nothing to offer, 1 its lists, 2 done
     __shared__ double base[128];
-    __shared__ uint32_t bounds[4][W];
+    __shared__ uint32_t bounds[2][W];
     __shared__ BeamCand heads[W];
     static_assert(W == 8, "");
     __shared__ int found;
@@ -327,21 +321,31 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     if (tid == 0) found = 0;
 
-    // a list is piece list / beams of row list % beams; the first keys of the thread's first one are on their way early
+    // a list is a piece of a row, the pieces of a row one after another; the first DEPTH keys of a list are a thread's
+    // each, and the first of these keys are on their way early.  Neighbours are mostly one row's, so the best row's wave
+    // alone gives a close bound
     const int lists = a.beams * w.n, n_out = a.n_out;
-    auto keys_of = [&](int list) { return w.keys + ((row0 + list % a.beams) * w.n + list / a.beams) * n_out; };
-    uint64_t ahead8[8];
-    auto load8 = [&](int list, int d0) {
-        const uint64_t *src = keys_of(list) + d0;
+    constexpr int DEPTH = 8, LISTS = BEAM_T2 / DEPTH, A = 4;
+    const int my_list = wave * (WAVE / DEPTH) + lane / DEPTH, my_depth = lane % DEPTH;
+    auto keys_of = [&](int list) { return w.keys + (row0 * w.n + list) * n_out; };
+    const double per_piece = 1.0 / w.n;
+    auto row_of = [&](int list) { return (int)(((double)list + 0.5) * per_piece); };  // half a piece away from the next row
+    uint64_t keys[A];
+    auto load_keys = [&](int l0, int d0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ahead8[j] = d0 + j < n_out ? src[j] : 0;
+        for (int j = 0; j < A; ++j) {
+            const int list = l0 + j * LISTS + my_list, d = d0 + my_depth;
+            keys[j] = list < lists && d < n_out ? keys_of(list)[d] : 0;
+        }
     };
-    if (tid < lists) load8(tid, 0);
+    load_keys(0, 0);
 
     // the rows' sums
     const ExpBelow exp_below;
     for (int r = wave; r < a.beams; r += W) {
         const BeamPiece *p = w.pieces + (row0 + r) * w.n;
+        const double score = a.scores[row0 + r];
+        const bool ended = a.done && a.done[row0 + r];
         float m = -INFINITY;
         for (int i = lane; i < w.n; i += WAVE) m = fmaxf(m, p[i].top);
 #pragma unroll
@@ -354,8 +358,7 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         }
         s = wave_sum(s);
         if (lane == 0) {
-            const double lse = s == 0. ? -INFINITY : (double)m + log(s), score = a.scores[row0 + r], b = score - lse;
-            const bool ended = a.done && a.done[row0 + r];
+            const double lse = s == 0. ? -INFINITY : (double)m + log(s), b = score - lse;
             base[r] = ended ? score : b;
             state[r] = fabs(base[r]) < INFINITY ? ended ? 2 : 1 : 0;
             if (a.lse) a.lse[row0 + r] = (float)lse;
@@ -365,45 +368,74 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
 
     // what a key of a list is worth; without one the key is 0
     auto worth = [&](int list, uint64_t key, bool first) {
-        BeamCand x = {0, 0, list % a.beams};
+        BeamCand x = {0, 0, row_of(list)};
         const int st = state[x.row];
         if (st == 1 && key) {
             x.key = key;
             x.c = order64(base[x.row] + (double)value32((uint32_t)(key >> 32)));
-        } else if (st == 2 && first && list < a.beams) {
+        } else if (st == 2 && first && list == x.row * w.n) {
             x.c = order64(base[x.row]);
             x.key = 1ull << 32 | (uint32_t)~a.end_token;
         }
         return x;
     };
     auto candidate = [&](int list, int d) { return worth(list, keys_of(list)[d], d == 0); };
-    // a bound that at least n_out candidates reach, from the first ones of the lists
-    const int depth = (n_out + lists - 1) / lists;
-    uint32_t most = tid < lists ? (uint32_t)(worth(tid, ahead8[0], true).c >> 32) : 0u;
-    for (int e = tid + BEAM_T2; e < lists * depth; e += BEAM_T2) most = max(most, (uint32_t)(candidate(e % lists, e / lists).c >> 32));
-    if (lists < BEAM_T2 && tid >= lists && tid < lists * depth) most = (uint32_t)(candidate(tid % lists, tid / lists).c >> 32);
+    // a bound that at least n_out candidates reach, from the keys that are here; of more lists, from each one's first,
+    // one list after another in another wave
+    uint32_t most = 0;
+    if (lists <= A * LISTS) {
+#pragma unroll
+        for (int j = 0; j < A; ++j)
+            if (j * LISTS + my_list < lists) most = max(most, (uint32_t)(worth(j * LISTS + my_list, keys[j], my_depth == 0).c >> 32));
+    } else {
+        for (int l = lane * W + wave; l < lists; l += BEAM_T2) most = max(most, (uint32_t)(worth(l, keys_of(l)[0], true).c >> 32));
+    }
     wave_bounds<22, W>(most, n_out, false, bounds);
     __syncthreads();
-    const uint32_t t = waves_bound<W>(bounds);
-    for (int l = tid; l < lists; l += BEAM_T2)
-        for (int d0 = 0; d0 < n_out; d0 += 8) {
-            if (l != tid || d0) load8(l, d0);
-            bool more = true;
+    uint32_t t = waves_bound<W>(bounds, n_out, false);
+    int n;
+    for (bool again = false;; again = true) {
+        // the candidates that reach it; a list all of whose keys here do has more to look at
+        bool deeper = false;
+        for (int d0 = 0; d0 < n_out; d0 += DEPTH) {
+            for (int l0 = 0; l0 < lists; l0 += A * LISTS) {
+                if (l0 || d0 || again) load_keys(l0, d0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const BeamCand x = worth(l, ahead8[j], d0 + j == 0);
-                more = x.key && (uint32_t)(x.c >> 32) >= t;
-                if (!more) continue;
-                const int at = atomicAdd(&found, 1);
-                if (at >= BEAM_CAP2) continue;
-                cs[at] = x.c;
-                ks[at] = x.key;
-                rs[at] = (uint8_t)x.row;
+                for (int j = 0; j < A; ++j) {
+                    const int list = l0 + j * LISTS + my_list;
+                    BeamCand x = {0, 0, 0};
+                    if (list < lists) x = worth(list, keys[j], d0 + my_depth == 0);
+                    const bool reach = x.key && (uint32_t)(x.c >> 32) >= t;
+                    const uint64_t m = __builtin_amdgcn_ballot_w64(reach);
+                    if (!m) continue;
+                    deeper |= reach && my_depth == DEPTH - 1;
+                    int at = 0;
+                    if (lane == 0) at = atomicAdd(&found, (int)__builtin_popcountll(m));
+                    at = __builtin_amdgcn_readfirstlane(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+                    if (reach && at < BEAM_CAP2) {
+                        cs[at] = x.c;
+                        ks[at] = x.key;
+                        rs[at] = (uint8_t)x.row;
+                    }
+                }
             }
-            if (!more) break;
+            if (!__syncthreads_or(deeper)) break;
+            deeper = false;
         }
-    __syncthreads();
-    const int n = found;
+        __syncthreads();
+        n = found;
+        if (n <= BEAM_CAP2) break;
+        // too many (few rows are alive): the candidates that are here give a higher bound
+        most = 0;
+        for (int i = tid; i < BEAM_CAP2; i += BEAM_T2) most = max(most, (uint32_t)(cs[i] >> 32));
+        wave_bounds<32, W>(most, n_out, true, bounds);
+        __syncthreads();
+        const uint32_t higher = waves_bound<W>(bounds, n_out, true);
+        if (higher <= t) break;
+        t = higher;
+        if (tid == 0) found = 0;
+        __syncthreads();
+    }
     const int64_t out0 = (int64_t)blockIdx.x * n_out;
     auto put = [&](int i, const BeamCand &x) {
         const bool none = x.key == 0;
@@ -468,8 +500,13 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
 
 // ---------------------------------------------------------------- launches
 
-// Values of a thread: pieces of 8192, or of 2048 where the larger ones would be too few for the chip.
-static int beam_values(int64_t rows, int64_t vocab) { if (const char *e = getenv("BV")) return atoi(e); return rows * ((vocab + 8191) / 8192) < 512 ? 8 : 32; }
+// Values of a thread: pieces of 8192, where these are too few for the chip of 4096 or 2048 (bf16, us for 8 / 16 / 32 values: one
+// row of 50257 12.3 / 13.2 / 14.6, 16 x 8 of 50257 24.5 / 24.5 / 23.1, 32 x 8 34 / 28.8 / 30.3, 2 x 32 of 131071 52 / 39 / 35).
+static int beam_values(int64_t rows, int64_t vocab)
+{
+    const int64_t large = rows * ((vocab + 8191) / 8192);
+    return large < 64 ? 8 : large < 256 ? 16 : 32;
+}
 
 static int beam_pieces(int64_t rows, int vocab)
 {

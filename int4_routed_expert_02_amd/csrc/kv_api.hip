@@ -303,7 +303,7 @@ extern "C" int moe_kv_copy(const moe_kv_shape *shape, const moe_kv_cache *cache,
 
 static int check_beam(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out)
 {
-    if (requests < 0 || beams < 1 || vocab < 1 || n_out < 1) return MOE_ERR_SHAPE;
+    if (requests < 0 || beams < 1 || vocab < 1 || vocab > 1 << 30 || n_out < 1) return MOE_ERR_SHAPE;
     if (beams > 128 || n_out > 128) return MOE_ERR_UNSUPPORTED;
     const int64_t rows = (int64_t)requests * beams;
     if (rows >= 1 << 22 || rows * vocab > (int64_t)1 << 36) return MOE_ERR_SHAPE;  // a launch below 2^32 lanes

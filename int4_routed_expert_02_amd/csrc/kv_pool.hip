@@ -58,11 +58,10 @@ struct ChunkBits {
 __device__ __forceinline__ ChunkBits chunk_live(const int32_t *refs, int64_t p0, int64_t n_pages, int lane)
 {
     int r[16];
+    const int32_t *at = refs + p0 + lane;
+    const int left = (int)min(max(n_pages - p0, (int64_t)0), (int64_t)CHUNK) - lane;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t p = p0 + 64 * i + lane;
-        r[i] = p < n_pages ? refs[p] : 0;
-    }
+    for (int i = 0; i < 16; ++i) r[i] = 64 * i < left ? at[64 * i] : 0;
     ChunkBits c;
     c.n = 0;
 #pragma unroll
@@ -303,8 +302,8 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
                 }
                 const int b = i - begin[lo], block = from[lo] + b;
                 // (the bounds hold for any tables with ascending row_start)
-                if (i < all && s0 + lo < a.n_seq && (unsigned)block < (unsigned)a.max_pages) f(s0 + lo, block, b == 0 && inside[lo]);
-                else f(-1, 0, false);
+                const bool is = i < all && s0 + lo < a.n_seq && (unsigned)block < (unsigned)a.max_pages;
+                f(is ? s0 + lo : -1, block, is && b == 0 && inside[lo]);  // one call for all lanes: f has barriers
             }
             __syncthreads();
         }
@@ -398,7 +397,151 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
     });
 }
 
+// The same in one launch where the wanted blocks are at most 1024 and the pages few: who shares a page is
+// found by comparing the blocks in LDS, the free pages are read on the way.
+constexpr int RESERVE_PAGES = 1 << 16;  // pages, at most: 4 KB of counts a wave
+
+__global__ __launch_bounds__(RT) void k_kv_reserve_small(KvArgs a, int32_t *__restrict__ pages, int32_t *__restrict__ refs,
+                                                         int32_t *__restrict__ copy_src, int32_t *__restrict__ copy_dst,
+                                                         int32_t *__restrict__ missing)
+{
+    __shared__ int begin[RT], from[RT], shared[RT], list[RT], waves[RT / WAVE];
+    __shared__ uint8_t inside[RT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    ChunkBits live = chunk_live(refs, wave * CHUNK, a.n_pages, lane);
+    Wanted w = {0, 0, false};
+    if (tid < a.n_seq) {
+        w = wanted_blocks(a, tid);
+        if (copy_src) copy_src[tid] = copy_dst[tid] = -1;
+        if (missing) missing[tid] = 0;
+    }
+    int all, need;
+    const int at = scan1024(w.n, waves, all);
+    all = min(all, RT);
+    begin[tid] = at;
+    from[tid] = w.first;
+    inside[tid] = w.partial;
+    __syncthreads();
+    // the thread's block
+    int s = 0, hi = RT, page = -1, held = 0;
+#pragma unroll 1
+    while (hi - s > 1) {
+        const int mid = (s + hi) / 2;
+        if (begin[mid] <= tid) s = mid;
+        else hi = mid;
+    }
+    const int block = from[s] + tid - begin[s];
+    const bool mine = tid < all && s < a.n_seq && (unsigned)block < (unsigned)a.max_pages;
+    const bool partial = mine && tid == begin[s] && inside[s];
+    if (mine) page = pages[(int64_t)s * a.max_pages + block];
+    if (in_cache(a, page)) held = refs[page];
+    else page = -1;
+    bool needs = mine && page < 0 && !partial;
+    shared[tid] = held > 1 ? page : -1;
+    if (__syncthreads_or(held > 1) && held > 1) {
+        int wanted = 0, leader = RT;
+#pragma unroll 4
+        for (int i = 0; i < all; ++i) {
+            const bool same = shared[i] == page;
+            wanted += same;
+            leader = same ? min(leader, i) : leader;
+        }
+        needs = wanted != held || leader != tid;
+    }
+    const int rank = scan1024(needs, waves, need);
+    // the lowest free pages, RT chunks' worth of waves at a time
+    int have = 0;
+#pragma unroll 1
+    for (int p0 = 0; p0 < a.n_pages && have < need; p0 += RT / WAVE * CHUNK) {
+        const int first = p0 + wave * CHUNK;
+        if (p0) live = chunk_live(refs, first, a.n_pages, lane);
+        const int there = min(max(a.n_pages - first, 0), CHUNK);
+        int total;
+        int to = have + scan1024(lane == 0 ? there - live.n : 0, waves, total);
+        to = __builtin_amdgcn_readfirstlane(to);
+        have += total;
+        if (there > live.n && to < need) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                uint64_t free = ~live.m[u];
+                const int rest = there - 64 * u;
+                if (rest < 64) free &= rest <= 0 ? 0ull : ~0ull >> (64 - rest);
+                const int i = to + below(free, lane);
+                if ((free >> lane & 1) && i < need) list[i] = first + 64 * u + lane;
+                to += __builtin_popcountll(free);
+            }
+        }
+    }
+    __syncthreads();
+    if (!mine) return;
+    const int got = needs && rank < have ? list[rank] : -1;
+    if (!needs) {
+        if (page < 0 && missing) atomicAdd(missing + s, 1);  // its older rows are gone
+        return;
+    }
+    pages[(int64_t)s * a.max_pages + block] = got;
+    if (page >= 0) atomicSub(refs + page, 1);
+    if (got < 0) {
+        if (missing) atomicAdd(missing + s, 1);
+        return;
+    }
+    refs[got] = 1;
+    if (page >= 0 && partial && copy_src) {
+        copy_src[s] = page;
+        copy_dst[s] = got;
+    }
+}
+
 // ---------------------------------------------------------------- moved together
+
+// All in one launch where pages and entries are few: the moves in LDS.
+constexpr int COMPACT_PAGES = RT / WAVE * CHUNK, COMPACT_ENTRIES = 1 << 14;
+
+__global__ __launch_bounds__(RT) void k_kv_compact_small(KvArgs a, int32_t *__restrict__ pages, int32_t *__restrict__ refs, int max_moves,
+                                                         int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *__restrict__ n_live)
+{
+    __shared__ uint16_t move[COMPACT_PAGES], hole[COMPACT_PAGES / 2];
+    __shared__ int waves[RT / WAVE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const ChunkBits live = chunk_live(refs, wave * CHUNK, a.n_pages, lane);
+    int all, moved;
+    int rank = __builtin_amdgcn_readfirstlane(scan1024(lane == 0 ? live.n : 0, waves, all));  // pages in use below the chunk
+    int movers = 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        const int p = wave * CHUNK + 64 * u + lane, r = rank + below(live.m[u], lane);
+        const bool used = live.m[u] >> lane & 1;
+        rank += __builtin_popcountll(live.m[u]);
+        int k = -1;
+        if (used && p >= all) {
+            k = all - 1 - r;
+            if (k < max_moves) src[k] = p;
+            ++movers;
+        } else if (!used && p < all && p - r < max_moves) {
+            hole[p - r] = (uint16_t)p;
+            dst[p - r] = p;
+        }
+        move[p] = (uint16_t)(k < max_moves ? k : -1);
+    }
+    scan1024(movers, waves, moved);
+    __syncthreads();
+    moved = min(moved, max_moves);
+    for (int i = moved + tid; i < max_moves; i += RT) src[i] = dst[i] = -1;
+    if (n_live && tid == 0) n_live[0] = all;
+    for (int i = tid; i < a.n_seq * a.max_pages; i += RT) {
+        const int page = pages[i];
+        if (!in_cache(a, page)) continue;
+        const int k = move[page];
+        if (k != 0xFFFF) pages[i] = hole[k];
+    }
+#pragma unroll 1
+    for (int u = 0; u < 16; ++u) {
+        const int p = wave * CHUNK + 64 * u + lane, k = move[p];
+        if (k == 0xFFFF) continue;
+        refs[hole[k]] = refs[p];
+        refs[p] = 0;
+    }
+}
 
 // First launch: pages in use of every block; the lists' empty state.
 __global__ __launch_bounds__(256) void k_kv_compact_count(const int32_t *__restrict__ refs, int n_pages, int steps, int max_moves,
@@ -589,6 +732,11 @@ hipError_t launch_kv_fork(const KvArgs &a, const int32_t *parent, int32_t *len_o
 hipError_t launch_kv_reserve(const KvArgs &a, int32_t *pages, int32_t *refs, int32_t *copy_src, int32_t *copy_dst, int32_t *missing,
                              void *ws, hipStream_t st)
 {
+    // rows lie in at most rows / P + 2 blocks of a sequence
+    if ((int64_t)(a.rows >> a.page_log2) + 2 * (int64_t)a.n_seq <= RT && a.n_pages <= RESERVE_PAGES) {
+        hipLaunchKernelGGL(k_kv_reserve_small, dim3(1), dim3(RT), 0, st, a, pages, refs, copy_src, copy_dst, missing);
+        return hipGetLastError();
+    }
     const PoolBlocks b = pool_blocks(a.n_pages);
     int32_t *counts = (int32_t *)ws, *list = (int32_t *)((char *)ws + list_at());
     PageUse *use = (PageUse *)((char *)ws + use_at(a.n_pages));
@@ -604,6 +752,10 @@ hipError_t launch_kv_reserve(const KvArgs &a, int32_t *pages, int32_t *refs, int
 hipError_t launch_kv_compact(const KvArgs &a, int32_t *pages, int32_t *refs, int max_moves, int32_t *src, int32_t *dst, int32_t *n_live,
                              void *ws, hipStream_t st)
 {
+    if (a.n_pages <= COMPACT_PAGES && (int64_t)a.n_seq * a.max_pages <= COMPACT_ENTRIES) {
+        hipLaunchKernelGGL(k_kv_compact_small, dim3(1), dim3(RT), 0, st, a, pages, refs, max_moves, src, dst, n_live);
+        return hipGetLastError();
+    }
     const PoolBlocks b = pool_blocks(a.n_pages);
     int32_t *counts = (int32_t *)ws, *move = (int32_t *)((char *)ws + list_at());
     const unsigned n = b.n ? b.n : 1;  // without a page: n_live 0

@@ -49,30 +49,71 @@ __device__ __forceinline__ int blocks_of(const KvArgs &a, int len)
 
 __device__ __forceinline__ bool in_cache(const KvArgs &a, int page) { return (unsigned)page < (unsigned)a.n_pages; }
 
-// Which of the CHUNK pages from p0 on are in use: bit l of m[i] is page p0 + 64 i + l.
+// Which of the CHUNK pages from p0 on are in use: bit l of word(u) is page p0 + 64 u + l, 0 from n_pages on.  Lane u
+// holds word u, so that loops over the words stay loops.
 struct ChunkBits {
-    uint64_t m[16];
+    uint32_t lo, hi;
     int n;
+    __device__ __forceinline__ uint64_t word(int u) const
+    {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, u) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)lo, u);
+    }
 };
 
 __device__ __forceinline__ ChunkBits chunk_live(const int32_t *refs, int64_t p0, int64_t n_pages, int lane)
 {
+    ChunkBits c = {0, 0, 0};
+    if (p0 >= n_pages) return c;
+    // every lane loads, past the end the last page: loads under a condition wait for one another (4.3 us for 16)
     int r[16];
-    const int32_t *at = refs + p0 + lane;
-    const int left = (int)min(max(n_pages - p0, (int64_t)0), (int64_t)CHUNK) - lane;
+    const int32_t *at = refs + p0;
+    const int last = (int)min(n_pages - p0, (int64_t)CHUNK) - 1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = 64 * i < left ? at[64 * i] : 0;
-    ChunkBits c;
-    c.n = 0;
+    for (int i = 0; i < 16; ++i) r[i] = at[min(64 * i + lane, last)];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        c.m[i] = __builtin_amdgcn_ballot_w64(r[i] > 0);
-        c.n += __builtin_popcountll(c.m[i]);
+        const uint64_t m = __builtin_amdgcn_ballot_w64(r[i] > 0 && 64 * i + lane <= last);
+        c.n += __builtin_popcountll(m);
+        c.lo = lane == i ? (uint32_t)m : c.lo;
+        c.hi = lane == i ? (uint32_t)(m >> 32) : c.hi;
     }
     return c;
 }
 
-__device__ __forceinline__ int below(uint64_t m, int lane) { return __builtin_popcountll(m & ((1ull << lane) - 1)); }
+// Bits of m below the lane's own.
+__device__ __forceinline__ int below(uint64_t m)
+{
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// Sum over the lanes up to each one's own (of a wave, or of each row of 16 lanes).
+template <bool ROW>
+__device__ __forceinline__ int lanes_scan(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4 and 8 lanes below in the row
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    if (ROW) return x;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // the last lane of rows 0 and 2 to rows 1 and 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
+    return x;
+}
+
+// Sum of the workgroup's values before mine (`total`: of all), T threads, T / 64 at most 16 waves.  `waves` has 16 places.
+template <int T>
+__device__ __forceinline__ int group_scan(int v, int *waves, int &total)
+{
+    constexpr int W = T / WAVE;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, x = lanes_scan<false>(v);
+    __syncthreads();
+    if (lane == 63) waves[wave] = x;
+    __syncthreads();
+    const int sums = lanes_scan<true>((lane & 15) < W ? waves[lane & 15] : 0);
+    total = __builtin_amdgcn_readlane(sums, W - 1);
+    const int before = __builtin_amdgcn_readlane(sums, max(wave - 1, 0));
+    return (wave ? before : 0) + x - v;
+}
 
 // ---------------------------------------------------------------- given back
 
@@ -98,29 +139,6 @@ __global__ __launch_bounds__(256) void k_kv_release(KvArgs a, int sinks, int32_t
 constexpr int FORK_ENTRIES = 2048;   // entries of a row that a workgroup takes at a time
 constexpr int FORK_PARTS = 256;      // workgroups of a row, at most
 
-// Sum of the block's values before mine (in `total` the sum of all); 256 threads.
-__device__ __forceinline__ int scan256(int v, int *waves, int &total)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < WAVE; d <<= 1) {
-        const int y = __shfl_up(x, d, WAVE);
-        if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 63) waves[wave] = x;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        before += w < wave ? waves[w] : 0;
-        total += waves[w];
-    }
-    return before + x - v;
-}
-
 // The first workgroup: lengths, slots and the slots' copies.  The others: a part of one
 // row's table each, as a continuation (its entries from the parent) and as a parent (its pages'
 // counts change by the continuations less one).
@@ -131,7 +149,7 @@ __global__ __launch_bounds__(256) void k_kv_fork(KvArgs a, const int32_t *__rest
 {
     __shared__ int first[KV_FORK_MAX];
     __shared__ uint16_t left[KV_FORK_MAX];
-    __shared__ int waves[4];
+    __shared__ int waves[16];
     const int tid = threadIdx.x, n = a.n_seq;
     auto parent_of = [&](int s) {
         const int p = parent[s];
@@ -152,7 +170,7 @@ __global__ __launch_bounds__(256) void k_kv_fork(KvArgs a, const int32_t *__rest
         int total = 0;
         for (int s0 = 0, at = 0; s0 < n; s0 += 256, at += total) {   // sequences that none goes on from
             const int s = s0 + tid, none = s < n && first[s] == INT32_MAX;
-            const int rank = scan256(none, waves, total);
+            const int rank = group_scan<256>(none, waves, total);
             if (none) left[at + rank] = (uint16_t)s;
         }
         __syncthreads();
@@ -160,7 +178,7 @@ __global__ __launch_bounds__(256) void k_kv_fork(KvArgs a, const int32_t *__rest
         for (int s0 = 0, at = 0; s0 < n; s0 += 256, at += total) {   // as many as there are sequences without a slot
             const int s = s0 + tid, p = s < n ? parent_of(s) : -1;
             const int extra = s < n && (p < 0 || first[p] != s);
-            const int rank = scan256(extra, waves, total);
+            const int rank = group_scan<256>(extra, waves, total);
             if (s >= n) continue;
             const int slot = slot_of(extra ? left[at + rank] : p);
             const bool copied = extra && p >= 0 && len_of(p) > 0;
@@ -248,28 +266,6 @@ __global__ __launch_bounds__(256) void k_kv_reserve_count(KvArgs a, const int32_
 // first; then how many pages are needed; their list; then the hand-out.
 constexpr int RT = 1024;
 
-__device__ __forceinline__ int scan1024(int v, int *waves, int &total)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < WAVE; d <<= 1) {
-        const int y = __shfl_up(x, d, WAVE);
-        if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 63) waves[wave] = x;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < RT / WAVE; ++w) {
-        before += w < wave ? waves[w] : 0;
-        total += waves[w];
-    }
-    return before + x - v;
-}
-
 __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int32_t *refs, int32_t *copy_src, int32_t *copy_dst,
                                                    int32_t *missing, const int32_t *counts, int32_t *list, PageUse *use,
                                                    int blocks, int steps)
@@ -286,7 +282,7 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
             const int s = s0 + tid;
             Wanted w = {0, 0, false};
             if (s < a.n_seq) w = wanted_blocks(a, s);
-            const int at = scan1024(w.n, waves, total);
+            const int at = group_scan<RT>(w.n, waves, total);
             const int all = total;
             begin[tid] = at;
             from[tid] = w.first;
@@ -322,7 +318,11 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
     __syncthreads();
 
     // Of a wanted block: 0 it has its page, 1 it needs one, 2 it needs one in another's place, 3 its older rows are gone.
+    // first: of all that name the page of another here, which then is left with `rest` entries.
+    bool first = false;
+    int rest = 0;
     auto state = [&](int s, int b, bool partial, int &page) {
+        first = false;
         page = entry(s, b);
         if (!in_cache(a, page)) {
             page = -1;
@@ -331,8 +331,9 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
         const int held = use[page].refs;
         if (held <= 1) return 0;
         const int wanted = __hip_atomic_load(&use[page].blocks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const unsigned long long leader = __hip_atomic_load(&use[page].leader, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        return wanted == held && leader == key(s, b) ? 0 : 2;
+        first = __hip_atomic_load(&use[page].leader, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == key(s, b);
+        rest = wanted == held ? 1 : held - wanted;
+        return wanted == held && first ? 0 : 2;
     };
     int need = 0;
     each([&](int s, int b, bool partial) {
@@ -340,14 +341,14 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
         const int st = s >= 0 ? state(s, b, partial, page) : 0;
         need += st == 1 || st == 2;
     });
-    scan1024(need, waves, need);
+    group_scan<RT>(need, waves, need);
 
     // the lowest `need` free pages
     int have = 0;
     if (need) {
         for (int b0 = 0; b0 < blocks; b0 += RT) {
             const int i = b0 + tid;
-            const int before = scan1024(i < blocks ? counts[i] : 0, waves, total);
+            const int before = group_scan<RT>(i < blocks ? counts[i] : 0, waves, total);
             if (i < blocks) base[i] = have + before;
             have += total;
         }
@@ -360,12 +361,12 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
             for (int c = 0; c < steps * BLOCK_WAVES && at < have; ++c) {
                 const int64_t p0 = (int64_t)i * steps * BLOCK + c * CHUNK;
                 const ChunkBits live = chunk_live(refs, p0, a.n_pages, lane);
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 16; ++u) {
                     const int64_t p = p0 + 64 * u;
-                    uint64_t free = ~live.m[u];
+                    uint64_t free = ~live.word(u);
                     if (p + 64 > a.n_pages) free &= p >= a.n_pages ? 0ull : ~0ull >> (64 - (int)(a.n_pages - p));
-                    const int mine = at + below(free, lane);
+                    const int mine = at + below(free);
                     if ((free >> lane & 1) && mine < have) list[mine] = (int32_t)(p + lane);
                     at += __builtin_popcountll(free);
                 }
@@ -380,14 +381,14 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
         int page = -1;
         const int st = s >= 0 ? state(s, b, partial, page) : 0;
         const bool needs = st == 1 || st == 2;
-        const int rank = given + scan1024(needs, waves, total);
+        const int rank = given + group_scan<RT>(needs, waves, total);
         given += total;
+        if (s >= 0 && first) refs[page] = rest;
         if (st == 0) return;
         const int got = needs && rank < have ? list[rank] : -1;
         if (got < 0 && missing) atomicAdd(missing + s, 1);
         if (st == 3) return;
         pages[(int64_t)s * a.max_pages + b] = got;
-        if (st == 2) atomicSub(refs + page, 1);
         if (got < 0) return;
         refs[got] = 1;
         if (st == 2 && partial && copy_src) {
@@ -398,29 +399,42 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
 }
 
 // The same in one launch where the wanted blocks are at most 1024 and the pages few: who shares a page is
-// found by comparing the blocks in LDS, the free pages are read on the way.
-constexpr int RESERVE_PAGES = 1 << 16;  // pages, at most: 4 KB of counts a wave
+// found by comparing the blocks in LDS, and a block finds its free page in the pages' bits there.
+constexpr int RESERVE_PAGES = 64 * RT;  // pages, at most: a word of bits for each thread
 
 __global__ __launch_bounds__(RT) void k_kv_reserve_small(KvArgs a, int32_t *__restrict__ pages, int32_t *__restrict__ refs,
                                                          int32_t *__restrict__ copy_src, int32_t *__restrict__ copy_dst,
                                                          int32_t *__restrict__ missing)
 {
-    __shared__ int begin[RT], from[RT], shared[RT], list[RT], waves[RT / WAVE];
+    __shared__ int begin[RT], from[RT], free_before[RT], waves[RT / WAVE];
+    __shared__ __align__(16) int shared[RT];
+    __shared__ uint64_t free_pages[RT];
     __shared__ uint8_t inside[RT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    ChunkBits live = chunk_live(refs, wave * CHUNK, a.n_pages, lane);
+#pragma unroll 1
+    for (int chunk = wave; chunk < RT / 16; chunk += RT / WAVE) {
+        const int p0 = chunk * CHUNK, rest = a.n_pages - p0 - 64 * lane;  // lane u: word u
+        if (p0 >= a.n_pages) {
+            if (lane < 16) free_pages[chunk * 16 + lane] = 0;
+            continue;
+        }
+        const ChunkBits live = chunk_live(refs, p0, a.n_pages, lane);
+        const uint64_t there = rest >= 64 ? ~0ull : rest <= 0 ? 0ull : ~0ull >> (64 - rest);
+        if (lane < 16) free_pages[chunk * 16 + lane] = ~((uint64_t)live.hi << 32 | live.lo) & there;
+    }
     Wanted w = {0, 0, false};
     if (tid < a.n_seq) {
         w = wanted_blocks(a, tid);
         if (copy_src) copy_src[tid] = copy_dst[tid] = -1;
         if (missing) missing[tid] = 0;
     }
-    int all, need;
-    const int at = scan1024(w.n, waves, all);
+    int all, have, total;
+    const int at = group_scan<RT>(w.n, waves, all);
     all = min(all, RT);
     begin[tid] = at;
     from[tid] = w.first;
     inside[tid] = w.partial;
+    free_before[tid] = group_scan<RT>((int)__builtin_popcountll(free_pages[tid]), waves, have);
     __syncthreads();
     // the thread's block
     int s = 0, hi = RT, page = -1, held = 0;
@@ -439,48 +453,51 @@ __global__ __launch_bounds__(RT) void k_kv_reserve_small(KvArgs a, int32_t *__re
     bool needs = mine && page < 0 && !partial;
     shared[tid] = held > 1 ? page : -1;
     if (__syncthreads_or(held > 1) && held > 1) {
-        int wanted = 0, leader = RT;
+        int wanted = 0, before = 0;
 #pragma unroll 4
-        for (int i = 0; i < all; ++i) {
-            const bool same = shared[i] == page;
-            wanted += same;
-            leader = same ? min(leader, i) : leader;
-        }
-        needs = wanted != held || leader != tid;
-    }
-    const int rank = scan1024(needs, waves, need);
-    // the lowest free pages, RT chunks' worth of waves at a time
-    int have = 0;
-#pragma unroll 1
-    for (int p0 = 0; p0 < a.n_pages && have < need; p0 += RT / WAVE * CHUNK) {
-        const int first = p0 + wave * CHUNK;
-        if (p0) live = chunk_live(refs, first, a.n_pages, lane);
-        const int there = min(max(a.n_pages - first, 0), CHUNK);
-        int total;
-        int to = have + scan1024(lane == 0 ? there - live.n : 0, waves, total);
-        to = __builtin_amdgcn_readfirstlane(to);
-        have += total;
-        if (there > live.n && to < need) {
+        for (int i = 0; i < all; i += 4) {
+            const u32x4 four = *(const u32x4 *)(shared + i);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                uint64_t free = ~live.m[u];
-                const int rest = there - 64 * u;
-                if (rest < 64) free &= rest <= 0 ? 0ull : ~0ull >> (64 - rest);
-                const int i = to + below(free, lane);
-                if ((free >> lane & 1) && i < need) list[i] = first + 64 * u + lane;
-                to += __builtin_popcountll(free);
+            for (int j = 0; j < 4; ++j) {
+                const bool same = (int)four[j] == page;
+                wanted += same;
+                before += same && i + j < tid;
             }
         }
+        needs = wanted != held || before;
+        // all that name it here get another page, but for the first where no one else holds it
+        if (!before) refs[page] = wanted == held ? 1 : held - wanted;
     }
-    __syncthreads();
+    const int rank = group_scan<RT>(needs, waves, total);
     if (!mine) return;
-    const int got = needs && rank < have ? list[rank] : -1;
+    int got = -1;
+    if (needs && rank < have) {
+        // the rank-th free page: its word, then its bit
+        int lo = 0, up = RT;
+#pragma unroll 1
+        while (up - lo > 1) {
+            const int mid = (lo + up) / 2;
+            if (free_before[mid] <= rank) lo = mid;
+            else up = mid;
+        }
+        uint64_t bits = free_pages[lo];
+        int left = rank - free_before[lo], bit = 0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const int below_d = __builtin_popcountll(bits & ((1ull << d) - 1));
+            if (left >= below_d) {
+                left -= below_d;
+                bits >>= d;
+                bit += d;
+            }
+        }
+        got = 64 * lo + bit;
+    }
     if (!needs) {
         if (page < 0 && missing) atomicAdd(missing + s, 1);  // its older rows are gone
         return;
     }
     pages[(int64_t)s * a.max_pages + block] = got;
-    if (page >= 0) atomicSub(refs + page, 1);
     if (got < 0) {
         if (missing) atomicAdd(missing + s, 1);
         return;
@@ -500,31 +517,44 @@ constexpr int COMPACT_PAGES = RT / WAVE * CHUNK, COMPACT_ENTRIES = 1 << 14;
 __global__ __launch_bounds__(RT) void k_kv_compact_small(KvArgs a, int32_t *__restrict__ pages, int32_t *__restrict__ refs, int max_moves,
                                                          int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *__restrict__ n_live)
 {
+    constexpr int STEPS = COMPACT_PAGES / RT;
     __shared__ uint16_t move[COMPACT_PAGES], hole[COMPACT_PAGES / 2];
-    __shared__ int waves[RT / WAVE];
+    __shared__ int before[COMPACT_PAGES / 64], waves[RT / WAVE];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const ChunkBits live = chunk_live(refs, wave * CHUNK, a.n_pages, lane);
-    int all, moved;
-    int rank = __builtin_amdgcn_readfirstlane(scan1024(lane == 0 ? live.n : 0, waves, all));  // pages in use below the chunk
-    int movers = 0;
+    // step i: pages RT i + tid
+    int held[STEPS];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        const int p = wave * CHUNK + 64 * u + lane, r = rank + below(live.m[u], lane);
-        const bool used = live.m[u] >> lane & 1;
-        rank += __builtin_popcountll(live.m[u]);
+    for (int i = 0; i < STEPS; ++i) held[i] = a.n_pages > 0 ? refs[min(RT * i + tid, a.n_pages - 1)] : 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        if (RT * i + tid >= a.n_pages) held[i] = 0;
+        const uint64_t m = __builtin_amdgcn_ballot_w64(held[i] > 0);
+        if (lane == 0) before[16 * i + wave] = __builtin_popcountll(m);
+    }
+    __syncthreads();
+    int all, moved, movers = 0;
+    const int at = group_scan<RT>(tid < COMPACT_PAGES / 64 ? before[tid] : 0, waves, all);
+    if (tid < COMPACT_PAGES / 64) before[tid] = at;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        if (RT * i >= a.n_pages) break;
+        const int p = RT * i + tid;
+        const bool used = held[i] > 0;
+        const int rank = before[16 * i + wave] + below(__builtin_amdgcn_ballot_w64(used));  // pages in use below p
         int k = -1;
         if (used && p >= all) {
-            k = all - 1 - r;
-            if (k < max_moves) src[k] = p;
             ++movers;
-        } else if (!used && p < all && p - r < max_moves) {
-            hole[p - r] = (uint16_t)p;
-            dst[p - r] = p;
+            k = all - 1 - rank;
+            if (k < max_moves) src[k] = p;
+            else k = -1;
+        } else if (!used && p < all && p - rank < max_moves) {
+            hole[p - rank] = (uint16_t)p;
+            dst[p - rank] = p;
         }
-        move[p] = (uint16_t)(k < max_moves ? k : -1);
+        move[p] = (uint16_t)k;
     }
-    scan1024(movers, waves, moved);
-    __syncthreads();
+    group_scan<RT>(movers, waves, moved);
     moved = min(moved, max_moves);
     for (int i = moved + tid; i < max_moves; i += RT) src[i] = dst[i] = -1;
     if (n_live && tid == 0) n_live[0] = all;
@@ -534,11 +564,11 @@ __global__ __launch_bounds__(RT) void k_kv_compact_small(KvArgs a, int32_t *__re
         const int k = move[page];
         if (k != 0xFFFF) pages[i] = hole[k];
     }
-#pragma unroll 1
-    for (int u = 0; u < 16; ++u) {
-        const int p = wave * CHUNK + 64 * u + lane, k = move[p];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int p = RT * i + tid, k = p < a.n_pages ? move[p] : 0xFFFF;
         if (k == 0xFFFF) continue;
-        refs[hole[k]] = refs[p];
+        refs[hole[k]] = held[i];
         refs[p] = 0;
     }
 }
@@ -597,12 +627,13 @@ __global__ __launch_bounds__(256) void k_kv_compact_plan(const int32_t *__restri
             r += w < wave ? waves[w] : 0;
             before += waves[w];
         }
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < 16; ++u) {
+            const uint64_t m = live.word(u);
             const int64_t p = p0 + 64 * u + lane;
-            const bool used = live.m[u] >> lane & 1;
-            const int rank = r + below(live.m[u], lane);
-            r += __builtin_popcountll(live.m[u]);
+            const bool used = m >> lane & 1;
+            const int rank = r + below(m);
+            r += __builtin_popcountll(m);
             if (p >= n_pages) continue;
             int to = -1;
             if (used && p >= all) {

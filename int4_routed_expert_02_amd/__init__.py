@@ -512,10 +512,11 @@ def moe_kv_read(sh: MoeKvShape, batch: MoeKvBatch, cache: MoeKvCache, k, v, stre
 
 def _ints(t, n, what):
     """Pointer of an int32 GPU tensor with n elements (None stays None)."""
-    torch = _torch or _bind_torch()
-    if t is not None and (t.dtype is not torch.int32 or t.numel() != n):
-        raise ValueError(f"{what} must be int32 with {n} elements")
-    return _ptr(t)
+    if t is None:
+        return None
+    if t.dtype is not (_torch or _bind_torch()).int32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 GPU tensor with {n} elements")
+    return t.data_ptr()
 
 
 def moe_kv_pool_workspace_bytes(sh: MoeKvShape) -> int:
@@ -525,7 +526,8 @@ def moe_kv_pool_workspace_bytes(sh: MoeKvShape) -> int:
 def moe_kv_release(sh: MoeKvShape, sink_tokens: int, kv_len, pages, refs, stream=None):
     """Give back the pages behind kv_len [n_seq] and those between the sinks and the shape's window (include/moe.h);
     pages [n_seq][max_pages] and refs [n_pages] are changed in place."""
-    _check(load().moe_kv_release(sh, sink_tokens, _ints(kv_len, sh.n_seq, "kv_len"), _ints(pages, sh.n_seq * sh.max_pages, "pages"),
+    n = sh.n_seq
+    _check(load().moe_kv_release(sh, sink_tokens, _ints(kv_len, n, "kv_len"), _ints(pages, n * sh.max_pages, "pages"),
                                  _ints(refs, sh.n_pages, "refs"), _stream(stream)), "moe_kv_release")
 
 
@@ -533,11 +535,11 @@ def moe_kv_fork(sh: MoeKvShape, batch: MoeKvBatch, parent, kv_len, pages, slots,
                 stream=None):
     """Sequence s goes on from parent[s] (include/moe.h): the batch's state before, kv_len, pages, slots and the lists of
     open pages to copy (slot_src, slot_dst) after; refs is changed in place.  slots and the lists may be None in 16 bits."""
-    n = sh.n_seq
+    n, blocks = sh.n_seq, sh.max_pages
     _, lens, table, slots_in = batch.sizes
-    if lens < n or table != (n, sh.max_pages) or (slots_in is not None and slots_in < n):
+    if lens < n or table != (n, blocks) or (slots_in is not None and slots_in < n):
         raise ValueError("the batch's tables do not fit the shape")
-    _check(load().moe_kv_fork(sh, batch, _ints(parent, n, "parent"), _ints(kv_len, n, "kv_len"), _ints(pages, n * sh.max_pages, "pages"),
+    _check(load().moe_kv_fork(sh, batch, _ints(parent, n, "parent"), _ints(kv_len, n, "kv_len"), _ints(pages, n * blocks, "pages"),
                               _ints(slots, n, "slots"), _ints(refs, sh.n_pages, "refs"), _ints(slot_src, n, "slot_src"),
                               _ints(slot_dst, n, "slot_dst"), _stream(stream)), "moe_kv_fork")
 

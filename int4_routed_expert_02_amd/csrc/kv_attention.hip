@@ -1080,6 +1080,14 @@ static int dec_parts(const KvArgs &a, int sinks)
     const int64_t tiles = len / 64 + 3, most = (tiles + DEC_WAVES - 1) / DEC_WAVES;
     const int64_t base = (int64_t)a.n_seq * a.kv_heads;
     int64_t ns = base > 0 ? (DEC_TARGET + base - 1) / base : 1;
+    if (sinks && base > 0) {
+        // Windows make the sequences alike, so parts only fill the chip: as many as run at once, one workgroup a
+        // compute unit with heads of 128 (32 x 8 key/value heads behind windows of 1024 and 3000: 20.6 and 38.9 us whole,
+        // 30.6 and 47.7 in two parts; 8 x 8 behind 2000: 15.9 in four parts, 22.7 in five), two with heads of 64; and
+        // a wave takes up to three tiles rather than wait for a join (32 x 4 behind 1024: 11.1 us, 12.3 in three parts).
+        ns = (a.head_dim == 128 ? 256 : 512) / base;
+        if (base >= 128 && tiles <= 3 * DEC_WAVES - 4) ns = 1;
+    }
     if (ns > most) ns = most;
     return (int)(ns < 1 ? 1 : ns);
 }

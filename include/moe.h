@@ -606,6 +606,7 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  * kv_len[s] (0: the sequence has ended), and with shape.window those that no row at
  * position kv_len[s] or later sees: block b with (b + 1) P <= kv_len[s] - window + 1 and
  * b P >= sink_tokens.  Their entries become -1, their pages' counts go down by one each.
+ * (Tokens dropped afterwards bring positions back into the window whose pages may be gone.)
  * pages and refs are changed in place.  max_len is not used.
  */
 int moe_kv_release(const moe_kv_shape *shape, int32_t sink_tokens, const int32_t *kv_len, int32_t *pages, int32_t *refs,

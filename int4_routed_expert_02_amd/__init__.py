@@ -215,14 +215,15 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_torch = _current = None  # torch, once a call has needed it, and the current stream's handle as torch keeps it
+# torch, once a call has needed it, the current stream's handle as torch keeps it, and the tables' type
+_torch = _current = _int32 = None
 
 
 def _bind_torch():
     """torch is imported by the first call that needs it, not with the package."""
-    global _torch, _current
+    global _torch, _current, _int32
     import torch
-    _torch = torch
+    _torch, _int32 = torch, torch.int32
     get_device = getattr(torch._C, "_cuda_getDevice", None)
     raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if get_device is not None and raw_stream is not None:
@@ -514,9 +515,11 @@ def _ints(t, n, what):
     """Pointer of an int32 GPU tensor with n elements (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not (_torch or _bind_torch()).int32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 GPU tensor with {n} elements")
-    return t.data_ptr()
+    if _int32 is None:
+        _bind_torch()
+    if t.dtype is _int32 and t.numel() == n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous int32 GPU tensor with {n} elements")
 
 
 def moe_kv_pool_workspace_bytes(sh: MoeKvShape) -> int:

@@ -5,10 +5,10 @@
 // logits.  First launch: a workgroup a piece of a row, the piece in registers.  Second launch: a workgroup a
 // request joins the pieces' sums and merges their lists.
 //
-// The n largest of a piece without sorting it: each wave finds the k-th largest of its 64 lanes' maxima
-// (a search over the leading bits of the value with ballots).  With k = n / g, rounded up, k lanes of each of
-// the g waves with the largest such bounds reach the g-th of them, so at least n values do, and few more.
-// These go to LDS, where each counts how many are ahead of it: its place.
+// The n largest of a piece without sorting it: each wave finds the k-th largest of its 64 lanes' maxima, k = n / waves
+// rounded up (a search over the leading bits of the value with ballots).  So at least n values reach the least
+// of the waves' bounds, and few more.  These go to LDS, where each counts how many are ahead of it: its place.
+// Where the waves are not alike (a row's last piece) their lanes are counted together, a barrier for each bit.
 //
 // The exponentials and their sums are 64 bits wide: a token's place among those of other rows hangs on the
 // difference of two log-sums, and 2^-24 of it changes places (one in some thousand steps with 32 beams).
@@ -96,34 +96,25 @@ __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
     return t;
 }
 
-// Two bounds of each wave, for g = W and for g = 1 (2 where n is above a wave's lanes): at least n of the values whose
-// largest of each lane is v reach what waves_bound() makes of them.  All waves together say most where their
-// values are alike (then the others are not looked at), one or two where the others have few.
+// A bound that n of the workgroup's values reach (v: the largest of each lane's), W waves.  Exactly: the n-th largest
+// lane, by a count over the workgroup for each bit.  0 where fewer lanes have a value.
 template <int BITS, int W>
-__device__ __forceinline__ void wave_bounds(uint32_t v, int n, bool alike, uint32_t (*bounds)[W])
+__device__ __forceinline__ uint32_t group_kth(uint32_t v, int n, int (*counts)[W])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t t = 0;
 #pragma unroll 1
-    for (int i = 0; i < (alike ? 1 : 2); ++i) {
-        const uint32_t b = wave_kth<BITS>(v, i == 0 ? (n + W - 1) / W : n > WAVE ? (n + 1) / 2 : n);
-        if (lane == 0) bounds[i][wave] = b;
-    }
-}
-
-template <int W>
-__device__ __forceinline__ uint32_t waves_bound(const uint32_t (*bounds)[W], int n, bool alike)
-{
-    uint32_t t = ~0u, first = 0, second = 0;
+    for (int b = 31; b > 31 - BITS; --b) {
+        const uint32_t trial = t | 1u << b;
+        const int c = __builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial));
+        if (lane == 0) counts[b & 1][wave] = c;
+        __syncthreads();  // (the other half is written next, this one again behind the next barrier)
+        int all = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) t = min(t, bounds[0][w]);
-    if (alike) return t;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const uint32_t b = bounds[1][w];
-        second = max(second, min(first, b));
-        first = max(first, b);
+        for (int w = 0; w < W; ++w) all += counts[b & 1][w];
+        if (all >= n) t = trial;
     }
-    return max(t, n > WAVE ? second : first);
+    return t;
 }
 
 // f(i, part, parts) for i < n, part < parts: as many lanes next to each other (`parts`, a power of two up to a wave) share
@@ -164,9 +155,8 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     __shared__ uint64_t cand[BEAM_CAP];
     __shared__ double sums[W];
     __shared__ float tops[W];
-    __shared__ uint32_t bounds[2][W];
-    __shared__ int found, counts[W];
-    static_assert(W == 4, "");
+    __shared__ uint32_t bounds[W];
+    __shared__ int found, counts[2][W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x / w.n;
     const int piece = blockIdx.x % w.n;
@@ -217,13 +207,16 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     sum = wave_sum(sum);
     if (!(wtop < INFINITY)) sum = __builtin_nan("");  // a NaN or +infinity among them
     const bool alike = N <= left;
-    wave_bounds<16, W>(order32(top), a.n_out, alike, bounds);
+    uint32_t bound = alike ? wave_kth<16>(order32(top), (a.n_out + W - 1) / W) : group_kth<16, W>(order32(top), a.n_out, counts);
     if (lane == 0) {
         sums[wave] = sum;
         tops[wave] = wtop;
+        bounds[wave] = bound;
     }
     __syncthreads();
-    const float t = value32(max(waves_bound<W>(bounds, a.n_out, alike), ORDER_FINITE));
+#pragma unroll
+    for (int i = 0; i < W; ++i) bound = min(bound, bounds[i]);
+    const float t = value32(max(bound, ORDER_FINITE));
     auto key = [&](int i) {
         return (uint64_t)order32(x[i]) << 32 | (uint32_t)~(uint32_t)(piece * N + tid * E + i / E * (BEAM_T1 * E) + i % E);
     };
@@ -257,10 +250,10 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, WAVE);
             __syncthreads();
-            if (lane == 0) counts[wave] = c;
+            if (lane == 0) counts[0][wave] = c;
             __syncthreads();
             c = 0;
-            for (int i = 0; i < W; ++i) c += counts[i];
+            for (int i = 0; i < W; ++i) c += counts[0][i];
             if (c >= a.n_out) bit_t = trial;
         }
         if (tid == 0) found = 0;
@@ -313,9 +306,9 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     __shared__ uint64_t cs[BEAM_CAP2], ks[BEAM_CAP2];
     __shared__ uint8_t rs[BEAM_CAP2], state[128];  // state of a row: 0 nothing to offer, 1 its lists, 2 done
     __shared__ double base[128];
-    __shared__ uint32_t bounds[2][W];
+    __shared__ uint32_t bounds[W];
+    __shared__ int counts[2][W];
     __shared__ BeamCand heads[W];
-    static_assert(W == 8, "");
     __shared__ int found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
@@ -390,9 +383,18 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     } else {
         for (int l = lane * W + wave; l < lists; l += BEAM_T2) most = max(most, (uint32_t)(worth(l, keys_of(l)[0], true).c >> 32));
     }
-    wave_bounds<22, W>(most, n_out, false, bounds);
-    __syncthreads();
-    uint32_t t = waves_bound<W>(bounds, n_out, false);
+    uint32_t t = 0;
+    if (n_out > 16) {
+        t = group_kth<22, W>(most, n_out, counts);
+    } else {
+        // few: the best wave's n_out-th lane says about as much, without barriers (4 beams: 7.3 us, 9.2 counted together;
+        // with n_out 64 of 8 x 16 beams the other way round, 13 and 40)
+        const uint32_t b = wave_kth<22>(most, n_out);
+        if (lane == 0) bounds[wave] = b;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) t = max(t, bounds[i]);
+    }
     int n;
     for (bool again = false;; again = true) {
         // the candidates that reach it; a list all of whose keys here do has more to look at
@@ -428,9 +430,7 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         // too many (few rows are alive): the candidates that are here give a higher bound
         most = 0;
         for (int i = tid; i < BEAM_CAP2; i += BEAM_T2) most = max(most, (uint32_t)(cs[i] >> 32));
-        wave_bounds<32, W>(most, n_out, true, bounds);
-        __syncthreads();
-        const uint32_t higher = waves_bound<W>(bounds, n_out, true);
+        const uint32_t higher = group_kth<32, W>(most, n_out, counts);
         if (higher <= t) break;
         t = higher;
         if (tid == 0) found = 0;

@@ -597,7 +597,8 @@ int moe_kv_read(const moe_kv_shape *shape, const moe_kv_batch *batch, const moe_
  *   refs  [n_pages] i32       how many entries of tables name each page; free: not above 0.  A
  *                             new pool is refs 0 and all entries -1.
  * One pool's tables and counts serve every layer whose cache has as many pages: the tables change
- * once, and moe_kv_copy carries the lists of copies out on each layer's cache.  Of the shape the
+ * once, and moe_kv_copy carries the lists of copies out on each layer's cache, in the order of the
+ * calls that wrote them.  Of the shape the
  * calls use n_seq, page_tokens, n_pages, max_pages, kv_bits and what is named below; all of it is
  * checked.  Counts that do not fit the tables give wrong pages but no access outside the buffers;
  * a call's outputs must not overlap its inputs unless it says so.

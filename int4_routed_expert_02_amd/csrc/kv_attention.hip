@@ -31,6 +31,11 @@
 // second halves not counted) for 3707 rows over 16384 and 8465 positions with heads of
 // 128, 400 for a causal prompt of 4096 rows with heads of 64, whose softmax is twice as
 // large a share.
+//
+// Sinks (positions that stay visible in front of a window) are a range of tiles of their own before the window's,
+// so a row's work goes by window and sinks: one row of 8 sequences of 75639..131072 positions, window 98304, 500 sinks,
+// 8 x 128 in 8 bits: 1.53 GB in 277 us, 5.5 TB/s; 32 sequences, window 1024, four sinks, 4 x 64: 12.6 us;
+// 3707 rows behind a window of 4096, 16 sinks, 8 x 128: 396 us, 630 TFLOP/s.
 #include "kv_device.h"
 
 namespace moe {

@@ -284,14 +284,17 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
     int total;
 
     // The wanted blocks one after another: f(sequence, block, whether it is its sequence's first and has older rows).
-    // Every thread calls f, those past the end with sequence -1.
+    // Every thread calls f, those past the end with sequence -1.  Rows that ascend lie in at most rows / P + 2 blocks of
+    // each sequence; whatever else the tables hold, no more than that are looked at.
     auto each = [&](auto f) {
+        int left = (a.rows >> a.page_log2) + 2 * a.n_seq;
         for (int s0 = 0; s0 < a.n_seq; s0 += RT) {
             const int s = s0 + tid;
             Wanted w = {0, 0, false};
             if (s < a.n_seq) w = wanted_blocks(a, s);
             const int at = group_scan<RT>(w.n, waves, total);
-            const int all = total;
+            const int all = min(total, left);
+            left -= max(all, 0);
             begin[tid] = at;
             from[tid] = w.first;
             inside[tid] = w.partial;
@@ -305,7 +308,6 @@ __global__ __launch_bounds__(RT) void k_kv_reserve(KvArgs a, int32_t *pages, int
                     else hi = mid;
                 }
                 const int b = i - begin[lo], block = from[lo] + b;
-                // (the bounds hold for any tables with ascending row_start)
                 const bool is = i < all && s0 + lo < a.n_seq && (unsigned)block < (unsigned)a.max_pages;
                 f(is ? s0 + lo : -1, block, is && b == 0 && inside[lo]);  // one call for all lanes: f has barriers
             }

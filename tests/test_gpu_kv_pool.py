@@ -207,6 +207,20 @@ def test_ids_outside_the_cache(n_pages):
     pool.release([3, 0, 0, 100, 2 ** 30])
 
 
+@pytest.mark.parametrize("n,n_pages", [(30, 500), (2000, 500), (2000, 90000)])
+def test_rows_that_do_not_ascend(n, n_pages):
+    """A table of rows that makes no sense: the call ends, and every entry and list names pages of the cache or none."""
+    rs = np.random.RandomState(n)
+    pool = Pool(PoolModel(n, 20, 16, n_pages, 16))
+    sh = pool.shape(3000, 3000)
+    src, dst, missing = (pool.junk(n) for _ in range(3))
+    for starts in (rs.randint(-5, 4000, n + 1), np.where(np.arange(n + 1) % 2, 3000, 0), np.arange(n + 1)[::-1]):
+        bt = moe.kv_batch(ints(starts), ints(rs.randint(-5, 400, n)), pool.pages)
+        moe.moe_kv_reserve(sh, bt, pool.pages, pool.refs, src, dst, missing, pool.ws(sh))
+        for t in (pool.pages, src, dst):
+            assert int(t.min()) >= -1 and int(t.max()) < n_pages
+
+
 def test_one_page_twice():
     """A row, or two rows, that name a page twice: it counts as often, and is parted like any other."""
     for bits in (8, 16):

@@ -45,8 +45,9 @@ __device__ __forceinline__ uint64_t order64(double x)
 
 __device__ __forceinline__ double value64(uint64_t o) { return __builtin_bit_cast(double, o ^ ((o >> 63) ? 1ull << 63 : ~0ull)); }
 
-// e^(x - top) for x <= top, top finite: (x - top) log2 e = k + f with a whole k and |f| <= 1/2, the polynomial of
-// degree 9 through 2^f at the Chebyshev points (2^-45.6 relative at most), times 2^k.  k comes from the low bits of a
+// e^(x - top) for x <= top, top finite: (x - top) log2 e = k + f with a whole k and |f| <= 1/2, 1 + f q(f) with the
+// polynomial q of degree 8 through (2^f - 1) / f at the Chebyshev points (2^-44.6 relative at most), times 2^k.  1 at x = top,
+// exactly: a row that allows one token has that logit as its log-sum, and equal scores stay equal.  k comes from the low bits of a
 // sum with 3 * 2^51 and goes into the result's exponent.  From e^-690 down (so -infinity too) it is e^-690, nothing
 // beside the 1 that the largest adds.  Positive NaN or infinity as x is the caller's.
 // The constants are kept in vector registers: the compiler otherwise moves them there for every value, a third
@@ -55,9 +56,9 @@ struct ExpBelow {
     double c[10], log2e, round, low;
     __device__ __forceinline__ ExpBelow()
     {
-        constexpr double C[10] = {0x1.000000000003dp+0, 0x1.62e42fefa39f7p-1, 0x1.ebfbdff8149f2p-3, 0x1.c6b08d7044119p-5,
-                                  0x1.3b2ab72b175eep-7, 0x1.5d87fe908f88ap-10, 0x1.43088e257f341p-13, 0x1.ffcb76789860fp-17,
-                                  0x1.63ef969a64d3cp-20, 0x1.b6571de2f2351p-24};
+        constexpr double C[10] = {1.0, 0x1.62e42fefa39efp-1, 0x1.ebfbdff823cedp-3, 0x1.c6b08d7047e52p-5,
+                                  0x1.3b2ab7181b755p-7, 0x1.5d87fe86fe88ep-10, 0x1.4308ac85aa947p-13, 0x1.ffcb9515a8016p-17,
+                                  0x1.63d136366db24p-20, 0x1.b63880a30e9ffp-24};
 #pragma unroll
         for (int i = 0; i < 10; ++i) c[i] = held(C[i]);
         log2e = held(0x1.71547652b82fep+0);

@@ -168,6 +168,26 @@ def test_small_differences():
     check(x, scores, 20)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,V,n", [(33, 31, 2), (16, 9000, 16), (4, 50257, 8)])
+def test_one_token_allowed(B, V, n, dtype):
+    """Rows that allow one token alone: its logit is the log-sum, so the beams keep their scores exactly and equal scores go
+    by the row, also beside ended beams.  (-20 - x and back lose nothing: x has 24 bits from 2^-19 on, the sum 53 below 2^6.)"""
+    import torch
+    x, scores = inputs(2, B, V, dtype, seed=B + V)
+    at = torch.randint(0, V, (2 * B, 1), device="cuda", generator=torch.Generator("cuda").manual_seed(V))
+    x = torch.full_like(x, -float("inf")).scatter(1, at, x.gather(1, at))
+    assert float(x[x > -float("inf")].abs().min()) > 1e-6 and float(x.max()) < 16
+    scores[:] = -20.0
+    scores[1, ::3] = -19.0
+    check(x, scores, n)
+    done = torch.zeros(2, B, dtype=torch.bool, device="cuda")
+    done[:, 1::2] = True
+    check(x, scores, n, done, 1)
+    out = call(x, scores, n)
+    assert set(out["score"].flatten().tolist()) <= {-20.0, -19.0, -float("inf")}
+
+
 @pytest.mark.parametrize("V,n", [(11, 6), (9000, 16), (50257, 40)])
 def test_done(V, n):
     """Ended beams stand still: end_token alone, at their score, also beside live ones and where all have ended."""

@@ -76,7 +76,8 @@ struct ExpBelow {
         const double t = __builtin_fma(d, log2e, round), f = __builtin_fma(d, log2e, round - t);
         double p = c[9];
 #pragma unroll
-        for (int i = 8; i >= 0; --i) p = __builtin_fma(p, f, c[i]);
+        for (int i = 8; i >= 1; --i) p = __builtin_fma(p, f, c[i]);
+        p = __builtin_fma(p, f, 1.0);
         u32x2 bits = __builtin_bit_cast(u32x2, p);
         bits[1] += __builtin_bit_cast(u32x2, t)[0] << 20;
         return __builtin_bit_cast(double, bits);
@@ -235,13 +236,18 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
         int at = 0;
         if (lane == 0) at = atomicAdd(&found, mine);
         at = __builtin_amdgcn_readfirstlane(at);
+        if (at + mine <= BEAM_CAP) {
+            // compared again: 32 masks of 64 lanes that are kept cost more than that
+            float again = t;
+            asm("" : "+s"(again));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint64_t m = __builtin_amdgcn_ballot_w64(x[i] >= t);
-            if (!m) continue;
-            const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-            if (x[i] >= t && to < BEAM_CAP) cand[to] = key(i);
-            at += __builtin_popcountll(m);
+            for (int i = 0; i < V; ++i) {
+                const bool reach = x[i] >= again;
+                const uint64_t m = __builtin_amdgcn_ballot_w64(reach);
+                if (!m) continue;
+                if (reach) cand[__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, at))] = key(i);
+                at += __builtin_popcountll(m);
+            }
         }
     }
     __syncthreads();
@@ -340,24 +346,29 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     };
     load_keys(0, 0);
 
-    // the rows' sums
+    // the rows' sums: as many lanes next to each other as a row has pieces, a wave at most
     const ExpBelow exp_below;
-    for (int r = wave; r < a.beams; r += W) {
-        const BeamPiece *p = w.pieces + (row0 + r) * w.n;
-        const double score = a.scores[row0 + r];
-        const bool ended = a.done && a.done[row0 + r];
+    int per = 1;
+    while (per < min(w.n, WAVE)) per *= 2;
+    for (int r0 = 0; r0 < a.beams; r0 += BEAM_T2 / per) {
+        const int r = r0 + tid / per, i0 = tid % per;
+        const bool live = r < a.beams;
+        const BeamPiece *p = w.pieces + (row0 + (live ? r : 0)) * w.n;
+        const double score = a.scores[row0 + (live ? r : 0)];
+        const bool ended = a.done && a.done[row0 + (live ? r : 0)];
         float m = -INFINITY;
-        for (int i = lane; i < w.n; i += WAVE) m = fmaxf(m, p[i].top);
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
+        for (int i = i0; i < w.n; i += per) m = fmaxf(m, p[i].top);
+#pragma unroll 1
+        for (int d = per / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
         double s = 0.;
-        for (int i = lane; i < w.n; i += WAVE) {
+        for (int i = i0; i < w.n; i += per) {
             const BeamPiece x = p[i];
             if (x.sum != x.sum) s = x.sum;
             else if (x.top > -INFINITY) s += x.sum * exp_below(x.top, m);
         }
-        s = wave_sum(s);
-        if (lane == 0) {
+#pragma unroll 1
+        for (int d = per / 2; d > 0; d >>= 1) s += __shfl_xor(s, d, WAVE);
+        if (live && i0 == 0) {
             const double lse = s == 0. ? -INFINITY : (double)m + log(s), b = score - lse;
             base[r] = ended ? score : b;
             state[r] = fabs(base[r]) < INFINITY ? ended ? 2 : 1 : 0;

@@ -15,9 +15,9 @@
 //
 // What bounds it.  Few rows: latency, two launches of 5 to 8 us (4 beams over 50257 tokens: 6.5 + 6.7 us).  Many: the vector
 // units.  A value takes 17 instructions of 64 bits for its exponential (a subtraction, the reduction, nine steps
-// of a polynomial, the exponent, the sum) and some 20 others, most of them for the values that reach the bound: 512
-// rows of 131071 f32 logits, 268 MB, 88 us (3.0 TB/s), 256 rows of 50257 in bf16 22 us, where a copy's rate
-// would take 52 and 5.
+// of a polynomial, the exponent, the sum) and some 19 others, most of them for the values that reach the bound: 512
+// rows of 131071 f32 logits, 268 MB, 86 us (3.1 TB/s; the instructions alone 61), 256 rows of 50257 in bf16 21 us, where a
+// copy's rate would take 52 and 5.
 #include "moe_device.h"
 #include "moe_launch.h"
 

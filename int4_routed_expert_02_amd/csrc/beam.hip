@@ -13,7 +13,7 @@
 // The exponentials and their sums are 64 bits wide: a token's place among those of other rows hangs on the
 // difference of two log-sums, and 2^-24 of it changes places (one in some thousand steps with 32 beams).
 //
-// What bounds it.  Few rows: latency, two launches of 5 to 8 us (4 beams over 50257 tokens: 6.5 + 6.7 us).  Many: the vector
+// What bounds it.  Few rows: latency, two launches of 5 to 8 us (4 beams over 50257 tokens: 7.6 + 6.1 us).  Many: the vector
 // units.  A value takes 17 instructions of 64 bits for its exponential (a subtraction, the reduction, nine steps
 // of a polynomial, the exponent, the sum) and some 19 others, most of them for the values that reach the bound: 512
 // rows of 131071 f32 logits, 268 MB, 86 us (3.1 TB/s; the instructions alone 61), 256 rows of 50257 in bf16 21 us, where a
@@ -91,6 +91,11 @@ __device__ __forceinline__ double wave_sum(double x)
     return x;
 }
 
+__device__ __forceinline__ int wave_reach(uint32_t v, uint32_t trial)
+{
+    return __builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial));
+}
+
 // The k-th largest of the wave's 64 values, rounded down to their BITS leading bits; k <= 64.
 template <int BITS>
 __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
@@ -99,22 +104,22 @@ __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int k)
 #pragma unroll 1
     for (int b = 31; b > 31 - BITS; --b) {
         const uint32_t trial = t | 1u << b;
-        if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial)) >= k) t = trial;
+        if (wave_reach(v, trial) >= k) t = trial;
     }
     return t;
 }
 
-// A bound that n of the workgroup's values reach (v: the largest of each lane's), W waves.  Exactly: the n-th largest
-// lane, by a count over the workgroup for each bit.  0 where fewer lanes have a value.
-template <int BITS, int W>
-__device__ __forceinline__ uint32_t group_kth(uint32_t v, int n, int (*counts)[W])
+// A bound that n of the workgroup's values reach, W waves: the n-th largest, to its BITS leading bits, by a count over the
+// workgroup for each.  wave_count(trial): how many of the wave's values reach it.  0 where there are fewer.
+template <int BITS, int W, typename F>
+__device__ __forceinline__ uint32_t group_kth(int n, int (*counts)[W], F wave_count)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t t = 0;
 #pragma unroll 1
     for (int b = 31; b > 31 - BITS; --b) {
         const uint32_t trial = t | 1u << b;
-        const int c = __builtin_popcountll(__builtin_amdgcn_ballot_w64(v >= trial));
+        const int c = wave_count(trial);
         if (lane == 0) counts[b & 1][wave] = c;
         __syncthreads();  // (the other half is written next, this one again behind the next barrier)
         int all = 0;
@@ -214,8 +219,23 @@ __global__ __launch_bounds__(BEAM_T1) void k_beam_piece(BeamSelect a, BeamWs w)
     }
     sum = wave_sum(sum);
     if (!(wtop < INFINITY)) sum = __builtin_nan("");  // a NaN or +infinity among them
-    const bool alike = N <= left;
-    uint32_t bound = alike ? wave_kth<16>(order32(top), (a.n_out + W - 1) / W) : group_kth<16, W>(order32(top), a.n_out, counts);
+    // the last piece of a row: its lanes' largest counted together, or where these are few for n_out, all its values (32
+    // bf16 rows of 9000 tokens, 100 of them: 21 us, 34 by the lanes; always all values: 128 of 2 x 128 x 131071 108 us, 100)
+    uint32_t bound;
+    if (N <= left) {
+        bound = wave_kth<16>(order32(top), (a.n_out + W - 1) / W);
+    } else if (2 * a.n_out <= min(left / E, BEAM_T1)) {
+        const uint32_t v = order32(top);
+        bound = group_kth<16, W>(a.n_out, counts, [&](uint32_t trial) { return wave_reach(v, trial); });
+    } else {
+        bound = group_kth<16, W>(a.n_out, counts, [&](uint32_t trial) {
+            const float y = value32(trial);  // (not a number below all numbers: the bound stays 0)
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(x[i] >= y));
+            return c;
+        });
+    }
     if (lane == 0) {
         sums[wave] = sum;
         tops[wave] = wtop;
@@ -327,12 +347,16 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     if (tid == 0) found = 0;
 
-    // a list is a piece of a row, the pieces of a row one after another; the first DEPTH keys of a list are a thread's
+    // a list is a piece of a row, the pieces of a row one after another; the first eight keys of a list are a thread's
     // each, and the first of these keys are on their way early.  Neighbours are mostly one row's, so the best row's wave
-    // alone gives a close bound
+    // alone gives a close bound.  Where lists are so few that more keys of each fit the threads, more are taken: a
+    // bound from eight keys of few lists lets most of all keys through (4 x 8 beams of 2000 tokens, 128 of them: 27 us, 198)
     const int lists = a.beams * w.n, n_out = a.n_out;
-    constexpr int DEPTH = 8, LISTS = BEAM_T2 / DEPTH, A = 4;
-    const int my_list = wave * (WAVE / DEPTH) + lane / DEPTH, my_depth = lane % DEPTH;
+    constexpr int A = 4;
+    int log_depth = 3;
+    while (log_depth < 6 && 1 << log_depth < n_out && lists << (log_depth + 1) <= BEAM_T2) ++log_depth;
+    const int depth = 1 << log_depth, at_once = BEAM_T2 >> log_depth;
+    const int my_list = tid >> log_depth, my_depth = tid & (depth - 1);
     auto keys_of = [&](int list) { return w.keys + (row0 * w.n + list) * n_out; };
     const double per_piece = 1.0 / w.n;
     auto row_of = [&](int list) { return (int)(((double)list + 0.5) * per_piece); };  // half a piece away from the next row
@@ -340,7 +364,7 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     auto load_keys = [&](int l0, int d0) {
 #pragma unroll
         for (int j = 0; j < A; ++j) {
-            const int list = l0 + j * LISTS + my_list, d = d0 + my_depth;
+            const int list = l0 + j * at_once + my_list, d = d0 + my_depth;
             keys[j] = list < lists && d < n_out ? keys_of(list)[d] : 0;
         }
     };
@@ -394,16 +418,16 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     // a bound that at least n_out candidates reach, from the keys that are here; of more lists, from each one's first,
     // one list after another in another wave
     uint32_t most = 0;
-    if (lists <= A * LISTS) {
+    if (lists <= A * at_once) {
 #pragma unroll
         for (int j = 0; j < A; ++j)
-            if (j * LISTS + my_list < lists) most = max(most, (uint32_t)(worth(j * LISTS + my_list, keys[j], my_depth == 0).c >> 32));
+            if (j * at_once + my_list < lists) most = max(most, (uint32_t)(worth(j * at_once + my_list, keys[j], my_depth == 0).c >> 32));
     } else {
         for (int l = lane * W + wave; l < lists; l += BEAM_T2) most = max(most, (uint32_t)(worth(l, keys_of(l)[0], true).c >> 32));
     }
     uint32_t t = 0;
     if (n_out > 16) {
-        t = group_kth<22, W>(most, n_out, counts);
+        t = group_kth<22, W>(n_out, counts, [&](uint32_t trial) { return wave_reach(most, trial); });
     } else {
         // few: the best wave's n_out-th lane says about as much, without barriers (4 beams: 7.3 us, 9.2 counted together;
         // with n_out 64 of 8 x 16 beams the other way round, 13 and 40)
@@ -417,18 +441,18 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     for (bool again = false;; again = true) {
         // the candidates that reach it; a list all of whose keys here do has more to look at
         bool deeper = false;
-        for (int d0 = 0; d0 < n_out; d0 += DEPTH) {
-            for (int l0 = 0; l0 < lists; l0 += A * LISTS) {
+        for (int d0 = 0; d0 < n_out; d0 += depth) {
+            for (int l0 = 0; l0 < lists; l0 += A * at_once) {
                 if (l0 || d0 || again) load_keys(l0, d0);
 #pragma unroll
                 for (int j = 0; j < A; ++j) {
-                    const int list = l0 + j * LISTS + my_list;
+                    const int list = l0 + j * at_once + my_list;
                     BeamCand x = {0, 0, 0};
                     if (list < lists) x = worth(list, keys[j], d0 + my_depth == 0);
                     const bool reach = x.key && (uint32_t)(x.c >> 32) >= t;
                     const uint64_t m = __builtin_amdgcn_ballot_w64(reach);
                     if (!m) continue;
-                    deeper |= reach && my_depth == DEPTH - 1;
+                    deeper |= reach && my_depth == depth - 1;
                     int at = 0;
                     if (lane == 0) at = atomicAdd(&found, (int)__builtin_popcountll(m));
                     at = __builtin_amdgcn_readfirstlane(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
@@ -446,9 +470,8 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         n = found;
         if (n <= BEAM_CAP2) break;
         // too many (few rows are alive): the candidates that are here give a higher bound
-        most = 0;
-        for (int i = tid; i < BEAM_CAP2; i += BEAM_T2) most = max(most, (uint32_t)(cs[i] >> 32));
-        const uint32_t higher = group_kth<32, W>(most, n_out, counts);
+        const uint32_t v0 = (uint32_t)(cs[tid] >> 32), v1 = (uint32_t)(cs[tid + BEAM_T2] >> 32);
+        const uint32_t higher = group_kth<32, W>(n_out, counts, [&](uint32_t trial) { return wave_reach(v0, trial) + wave_reach(v1, trial); });
         if (higher <= t) break;
         t = higher;
         if (tid == 0) found = 0;
@@ -476,9 +499,11 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
                     equal += c == mine;
                 }
                 if (equal > (i % parts == part)) {
-                    const BeamCand x = {mine, ks[i], rs[i]};
+                    const uint64_t key = ks[i];
+                    const int row = rs[i];
+#pragma unroll 4
                     for (int j = part; j < n; j += parts)
-                        if (cs[j] == mine) ahead += BeamCand{mine, ks[j], rs[j]}.ahead_of(x);
+                        ahead += (cs[j] == mine) & ((rs[j] < row) | ((rs[j] == row) & (ks[j] > key)));
                 }
                 return ahead;
             },
@@ -518,12 +543,16 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
 
 // ---------------------------------------------------------------- launches
 
-// Values of a thread: pieces of 8192, where these are too few for the chip of 4096 or 2048 (bf16, us for 8 / 16 / 32 values: one
-// row of 50257 12.3 / 13.2 / 14.6, 16 x 8 of 50257 24.5 / 24.5 / 23.1, 32 x 8 34 / 28.8 / 30.3, 2 x 32 of 131071 52 / 39 / 35).
+// Values of a thread: pieces of 8192, where these are too few for the chip of 4096 (bf16, us for 16 / 32 values: one row of
+// 131071 13.3 / 14.3, 4 x 4 of 50257 16.8 / 19.0, 32 x 8 26.5 / 26.5, 2 x 32 of 131071 35.6 / 29.7), and half or a quarter of
+// that where it saves a fifth of the places in a row's last piece (128 x 8 of 2000, 8 / 16 / 32 values: 14.9 / 16.7 / 20.2, of
+// 4000 18.7 / 16.3 / 19.8, of 12000 34.4 / 27.6 / 28.4).
 static int beam_values(int64_t rows, int64_t vocab)
 {
-    const int64_t large = rows * ((vocab + 8191) / 8192);
-    return large < 64 ? 8 : large < 256 ? 16 : 32;
+    auto padded = [&](int v) { return (vocab + BEAM_T1 * v - 1) / (BEAM_T1 * v) * (BEAM_T1 * v); };
+    int v = rows * ((vocab + 8191) / 8192) < 256 ? 16 : 32;
+    while (v > 8 && padded(v / 2) * 5 <= padded(v) * 4) v /= 2;
+    return v;
 }
 
 static int beam_pieces(int64_t rows, int vocab)

@@ -188,6 +188,20 @@ def test_one_token_allowed(B, V, n, dtype):
     assert set(out["score"].flatten().tolist()) <= {-20.0, -19.0, -float("inf")}
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,B,V,n", [(16, 2, 9000, 100), (4, 8, 2000, 128), (16, 16, 4000, 64), (64, 1, 50257, 64), (1, 2, 50257, 128),
+                                     (3, 1, 1105, 128), (2, 3, 808, 100), (5, 2, 129, 128), (300, 2, 8193, 120), (1, 4, 2176, 65)])
+def test_many_of_few_pieces(R, B, V, n, dtype):
+    """Many asked for where rows have few pieces, or a last one with few values; with values that are equal, and masked ones."""
+    import torch
+    x, scores = inputs(R, B, V, dtype, seed=V + n)
+    check(x, scores, n)
+    # equal values: the rows' sums of exponentials in any order are apart by less than the scores, which differ from row to row
+    check((x / 2).round() * 2, scores, n)
+    x[torch.rand(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(n)) < 0.95] = -float("inf")
+    check(x, scores, n)
+
+
 @pytest.mark.parametrize("V,n", [(11, 6), (9000, 16), (50257, 40)])
 def test_done(V, n):
     """Ended beams stand still: end_token alone, at their score, also beside live ones and where all have ended."""

@@ -1073,26 +1073,42 @@ __global__ __launch_bounds__(256) void k_attn_parts_few(KvArgs a, KvAttend t)
 // ---------------------------------------------------------------- launches
 
 constexpr int DEC_TARGET = 512;  // workgroups that fill the chip: 2 per compute unit
+constexpr int DEC_UNITS = 256;   // compute units
+
+// Rounds of a part's waves over its tiles, of `tiles` cut into `parts`.
+static int64_t dec_rounds(int64_t tiles, int64_t parts) { return ((tiles + parts - 1) / parts + DEC_WAVES - 1) / DEC_WAVES; }
+
+// Parts behind a window with sinks.  Windows make the sequences alike, so parts only fill the chip: as many as run at once,
+// one workgroup a compute unit.  A second one there costs more than its parts save (us for one row with heads of 64 in 8 bits
+// behind 4096: 192 key/value heads whole 28.7, in two parts 29.6; 8 rows 37.4 and 46.9; heads of 128 42.4 and 51.7).
+// And the parts have to save rounds worth their join, which costs 1.5 to 3 us: a round is 1.2 to 2.5 us with heads of 64 in
+// 8 bits, 3 and more with other heads and bits (128 key/value heads, whole and in two parts, behind 1024: 11.4 / 11.8 saving one
+// round with heads of 64 in 8 bits, 15.3 / 14.3 in 16, 17.8 / 17.0 with heads of 128 in 8 bits, 23.3 / 20.8 in 16; behind 2048,
+// saving two: 17.0 / 15.5, 22.3 / 19.5, 25.8 / 22.4, 37.1 / 28.6).  Over 720 calls of 8 to 384 key/value heads,
+// windows of 300 to 8192 and 1 and 8 rows, the parts taken here cost 1% more than the best ones; most where a few more
+// parts than compute units would run (160 heads of 64 behind 8192: 47.8 us whole, 36.3 in three parts).
+static int window_parts(const KvArgs &a, int sinks, int64_t len)
+{
+    int64_t span = len;  // positions between the first and the last that some row sees, behind the sinks
+    if (a.causal && span > (int64_t)a.window + a.max_rows - 1) span = (int64_t)a.window + a.max_rows - 1;
+    int64_t tiles = (span + 62) / 64 + 1 + ((int64_t)(sinks < len ? sinks : len) + 63) / 64;
+    if (tiles > (len + 63) / 64) tiles = (len + 63) / 64;
+    const int64_t base = (int64_t)a.n_seq * a.kv_heads, most = (tiles + DEC_WAVES - 1) / DEC_WAVES;
+    int64_t ns = base > 0 ? DEC_UNITS / base : 1;
+    if (ns > most) ns = most;
+    const int saved = a.head_dim == 64 && a.kv_bits == 8 ? 2 : 1;
+    return ns > 1 && dec_rounds(tiles, 1) - dec_rounds(tiles, ns) >= saved ? (int)ns : 1;
+}
 
 // Parts that a sequence's tiles may be cut into, so that few sequences still fill the chip.
 static int dec_parts(const KvArgs &a, int sinks)
 {
     int64_t len = a.max_len < ((int64_t)a.max_pages << a.page_log2) ? a.max_len : (int64_t)a.max_pages << a.page_log2;
-    if (a.window && a.causal) {
-        const int64_t span = (int64_t)a.window + a.max_rows + (sinks ? (int64_t)sinks + 64 : 0);
-        if (len > span) len = span;
-    }
+    if (sinks) return window_parts(a, sinks, len);
+    if (a.window && a.causal && len > (int64_t)a.window + a.max_rows) len = (int64_t)a.window + a.max_rows;
     const int64_t tiles = len / 64 + 3, most = (tiles + DEC_WAVES - 1) / DEC_WAVES;
     const int64_t base = (int64_t)a.n_seq * a.kv_heads;
     int64_t ns = base > 0 ? (DEC_TARGET + base - 1) / base : 1;
-    if (sinks && base > 0) {
-        // Windows make the sequences alike, so parts only fill the chip: as many as run at once, one workgroup a
-        // compute unit with heads of 128 (32 x 8 key/value heads behind windows of 1024 and 3000: 20.6 and 38.9 us whole,
-        // 30.6 and 47.7 in two parts; 8 x 8 behind 2000: 15.9 in four parts, 22.7 in five), two with heads of 64; and
-        // a wave takes up to three tiles rather than wait for a join (32 x 4 behind 1024: 11.1 us, 12.3 in three parts).
-        ns = (a.head_dim == 128 ? 256 : 512) / base;
-        if (base >= 128 && tiles <= 3 * DEC_WAVES - 4) ns = 1;
-    }
     if (ns > most) ns = most;
     return (int)(ns < 1 ? 1 : ns);
 }

@@ -690,9 +690,9 @@ int moe_kv_copy(const moe_kv_shape *shape, const moe_kv_cache *cache, int32_t n_
  * beams + beam of the logits gives its tokens v the sums
  *   c(r, v) = (scores[r] - lse_r) + logits[r][v],   lse_r = log sum_v exp(logits[r][v]),
  * taken in 64 bits from the inputs' values, since a token's place among those of another row
- * hangs on the difference of two such sums.  lse_r is off by 2^-43 and 2^-52 of itself at most
- * (exact where a row allows one token alone, equal for equal rows), so sums of unlike rows may change places where they are
- * closer than that.  A row with done[r] offers end_token alone, at
+ * hangs on the difference of two such sums.  lse_r is off by 2^-42 (above 2^28 tokens 2^-41) and 2^-52 of itself at
+ * most (exact where a row allows one token alone, equal for equal rows), so sums of unlike rows may change places where
+ * they are closer than that, or than a step of the 64-bit sums.  A row with done[r] offers end_token alone, at
  * scores[r].  Of a request's rows the n_out largest sums are taken in descending order; equal
  * sums: the lower row first, in one row the larger logit, then the lower token.  Logits of -infinity are
  * not offered, nor is anything by a row whose scores[r] - lse_r is not finite (all logits

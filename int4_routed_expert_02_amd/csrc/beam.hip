@@ -47,11 +47,15 @@ __device__ __forceinline__ double value64(uint64_t o) { return __builtin_bit_cas
 
 // e^(x - top) for x <= top, top finite: (x - top) log2 e = k + f with a whole k and |f| <= 1/2, 1 + f q(f) with the
 // polynomial q of degree 8 through (2^f - 1) / f at the Chebyshev points (2^-44.6 relative at most), times 2^k.  1 at x = top,
-// exactly: a row that allows one token has that logit as its log-sum, and equal scores stay equal.  k comes from the low bits of a
-// sum with 3 * 2^51 and goes into the result's exponent.  From e^-690 down (so -infinity too) it is e^-690, nothing
-// beside the 1 that the largest adds.  Positive NaN or infinity as x is the caller's.
-// The constants are kept in vector registers: the compiler otherwise moves them there for every value, a third
-// of the loop's instructions.
+// exactly: a row that allows one token has that logit as its log-sum.  (Its sum (score - x) + x is the score to a step of 64
+// bits, and the score itself where score - x loses nothing: where both lie between 2^-24 and 2^5, say.)  k comes from the low bits of a sum with 3 * 2^51 and goes into the result's exponent.  From e^-690 down (so -infinity
+// too) it is e^-690, nothing beside the 1 that the largest adds.  Positive NaN or infinity as x is the caller's.
+// A row's log-sum takes it three times (value to wave, wave to piece, piece to row), 3 * 2^-44.62 = 0.98 * 2^-43 of the sum; the
+// additions are a thread's 31, 6 and 4 over a wave and a piece and, of the row's pieces of 8192, one after another every 64th:
+// under 2^-47 up to 2^19 tokens, 0.5 * 2^-43 at 2^28, 2.05 * 2^-43 at 2^30; the rest (f's constant, the logarithm) under 2^-46.  So
+// 2^-42 up to 2^28 tokens, 2^-41 above, beside 2^-52 of the log-sum itself.
+// The constants are made once and stay in scalar registers: as literals the compiler moves them there again for every value, a
+// third of the loop's instructions, and in vector registers they leave fewer waves (119 us against 105 at 16 x 32 x 131071).
 struct ExpBelow {
     double c[10], log2e, round, low;
     __device__ __forceinline__ ExpBelow()
@@ -429,8 +433,9 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
     if (n_out > 16) {
         t = group_kth<22, W>(n_out, counts, [&](uint32_t trial) { return wave_reach(most, trial); });
     } else {
-        // few: the best wave's n_out-th lane says about as much, without barriers (4 beams: 7.3 us, 9.2 counted together;
-        // with n_out 64 of 8 x 16 beams the other way round, 13 and 40)
+        // few: the best wave's n_out-th lane says about as much, without barriers.  Both ways, counted together / the best
+        // wave: 16 of 4 x 50257 16.8 / 14.8 us, of 32 x 8 x 50257 29.4 / 27.8, of 8 x 16 x 50257 23.3 / 21.9; 20 of them 17.1 / 14.9,
+        // 29.4 / 28.9, 23.6 / 25.6; 64 of them 19.7 / 24.6, 36.8 / 188, 27.2 / 156
         const uint32_t b = wave_kth<22>(most, n_out);
         if (lane == 0) bounds[wave] = b;
         __syncthreads();
@@ -513,7 +518,10 @@ __global__ __launch_bounds__(BEAM_T2) void k_beam_request(BeamSelect a, BeamWs w
         for (int i = n + tid; i < n_out; i += BEAM_T2) put(i, BeamCand{0, 0, 0});
         return;
     }
-    // very many equal sums: the lists merged one candidate at a time
+    // very many equal sums: the lists merged one candidate at a time, each round from the lists' beginnings.  Inputs that
+    // get here have more than 1024 sums alike in 32 bits: 16 x 32 rows of 131071 that allow three tokens, the others at the
+    // type's lowest value, 64 asked for 427 us (94 where the logits differ), 128 rows with 128 asked for 1.2 ms (75); all
+    // logits equal 1.2 and 2.9 ms
     BeamCand last = {~0ull, ~0ull, -1};
     for (int i = 0; i < n_out; ++i) {
         BeamCand best = {0, 0, 0};

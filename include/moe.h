@@ -559,7 +559,8 @@ int moe_kv_attention(const moe_kv_shape *shape, const moe_kv_batch *batch, const
                      void *stream);
 
 /* Bytes of workspace moe_kv_attention needs for this shape (0 for an invalid shape, at
- * least 256 otherwise).  It grows with rows, q_heads and, below a bound, max_len. */
+ * least 256 otherwise).  It grows with rows, q_heads and, below a bound, max_len, but a call of fewer
+ * sequences or rows may be cut into more parts and need more: ask for every shape that is used. */
 size_t moe_kv_workspace_bytes(const moe_kv_shape *shape);
 
 /*
@@ -576,7 +577,8 @@ int moe_kv_attention_sinks(const moe_kv_shape *shape, int32_t sink_tokens, const
                            const moe_kv_cache *cache, const moe_bf16 *q, int64_t q_row_stride, void *out, float *lse,
                            void *ws, size_t ws_bytes, void *stream);
 
-/* Bytes of workspace moe_kv_attention_sinks needs (0 for an invalid shape or count, at least 256 otherwise). */
+/* Bytes of workspace moe_kv_attention_sinks needs (0 for an invalid shape or count, at least 256 otherwise).  As there a
+ * call of fewer sequences or rows may need more: ask for every shape that is used. */
 size_t moe_kv_attention_sinks_workspace_bytes(const moe_kv_shape *shape, int32_t sink_tokens);
 
 /*
@@ -642,7 +644,11 @@ int moe_kv_fork(const moe_kv_shape *shape, const moe_kv_batch *batch, const int3
  * copy_dst[s] are the copy that brings them into the new page (moe_kv_copy, before the append);
  * -1 otherwise (in 8 bits these rows are in the slot).  A block that finds no free page has entry
  * -1 afterwards, and one whose rows before the new ones are gone with their page stays at -1: such
- * blocks of sequence s are counted in missing[s], the append leaves their rows out.
+ * blocks of sequence s are counted in missing[s], the append leaves their rows out.  Where such a
+ * block had a page that others name too, the sequence gives up its share of it, and the rows of
+ * the block before the new ones are lost to the sequence for good (as are, in 8 bits, those in its slot).
+ * A program that frees pages then and goes on copies pages and refs before the call and, where
+ * a missing[s] is not 0, puts them back before any copy or append: nothing else has changed.
  *   pages, refs        changed in place (batch->pages is not used)
  *   copy_src, copy_dst [n_seq], kv_bits 16 (may be NULL with 8, and are not written then)
  *   missing            [n_seq], nullable

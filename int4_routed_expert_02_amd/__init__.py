@@ -561,9 +561,11 @@ def moe_kv_reserve(sh: MoeKvShape, batch: MoeKvBatch, pages, refs, copy_src=None
 
 
 def moe_kv_compact(sh: MoeKvShape, pages, refs, copy_src, copy_dst, n_live=None, ws=None, stream=None):
-    """Move the pages in use to the lowest ids, as many as copy_src and copy_dst have room for (include/moe.h); pages and
-    refs are changed in place, n_live [1] or None."""
-    moves = copy_src.numel()
+    """Move the pages in use to the lowest ids, as many as copy_src and copy_dst have room for (include/moe.h; None: no moves);
+    pages and refs are changed in place, n_live [1] or None."""
+    if (copy_src is None) != (copy_dst is None):
+        raise ValueError("a list's sources and destinations come together")
+    moves = copy_src.numel() if copy_src is not None else 0
     _check(load().moe_kv_compact(sh, _ints(pages, sh.n_seq * sh.max_pages, "pages"), _ints(refs, sh.n_pages, "refs"), moves,
                                  _ints(copy_src, moves, "copy_src"), _ints(copy_dst, moves, "copy_dst"), _ints(n_live, 1, "n_live"),
                                  _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)), "moe_kv_compact")
@@ -590,6 +592,8 @@ def moe_beam_select(logits, scores, parent, token, score, lse=None, done=None, d
     possibly apart), scores [requests][beams] f32; parent, token (int32) and score (f32) [requests][n_out]; lse
     [requests][beams] f32, done [requests][beams] and done_out [requests][n_out] (bool or uint8), each or None."""
     torch = _torch or _bind_torch()
+    if scores.dim() != 2 or parent.dim() != 2:
+        raise ValueError("scores must be [requests][beams] and parent [requests][n_out]")
     (requests, beams), n_out, f32 = scores.shape, parent.shape[1], torch.float32
     if logits.dim() != 2 or logits.shape[0] != requests * beams or logits.dtype not in (f32, torch.bfloat16) or not logits.is_cuda:
         raise ValueError("logits must be a float32 or bfloat16 [requests * beams][vocab] GPU tensor")
